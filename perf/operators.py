@@ -334,7 +334,7 @@ def run(s):
         return s["dx"]
     if op == "dispatch":
         qg.qg_sort_by_expert(s["ids"], s["offsets"], s["src"], s["pos"], workspace=s["scratch"])
-        qg.qg_gather_rows(s["x"], s["offsets"], s["src"], s["xs"], topk=c["topk"])
+        qg.qg_spread_rows(s["x"], s["pos"], s["xs"])
         return {"offsets": s["offsets"], "src": s["src"], "pos": s["pos"], "xs": s["xs"]}
     if op == "combine":
         qg.qg_combine_rows(s["ys"], s["pos"], s["y"], weights=s["weights"])
