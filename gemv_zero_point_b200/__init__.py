@@ -11,7 +11,9 @@ The function names are those of the C ABI:
   quantize_rows_a8, pack_w4_g32, qgemm_a8w4_f32,
   qgemm_pack_b_s8, qgemm_s8s8_requant, qgemm_s8s8_requant_packed,
   qconv2d_s8_im2col, qg_requant_params, qg_device_status,
-  quantize_rows_a8_sym, qconv2d_f32_dyn_a8w4
+  quantize_rows_a8_sym, qconv2d_f32_dyn_a8w4,
+  qgemm_a16w4_bf16, qgemm_a16w4_bf16_experts,
+  qg_sort_by_expert, qg_spread_rows, qg_combine_rows, qg_combine_rows_grad
 plus the *_bytes / *_workspace_bytes size queries.
 """
 from __future__ import annotations
@@ -108,6 +110,15 @@ _sig("pack_w4_g32_bf16_bytes", _sz, [_i32, _i32])
 _sig("pack_w4_g32_bf16", _i32, [_i32, _i32, _vp, _i64, _vp, _vp, _sz, _vp])
 _sig("qgemm_a8w4_f32_bf16s", _i32, [_i32, _i32, _i32, _vp, _i64, _vp, _vp, _f32, _f32, _vp,
                                     _i64, _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("qgemm_a16w4_bf16", _i32, [_i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _vp])
+_sig("qgemm_a16w4_bf16_experts", _i32, [_i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _vp,
+                                        _i64, _i32, _vp, _vp, _i64, _vp])
+_sig("qg_sort_by_expert_workspace_bytes", _sz, [_i32, _i32, _i32])
+_sig("qg_sort_by_expert", _i32, [_i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("qg_spread_rows", _i32, [_i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp])
+_sig("qg_combine_rows", _i32, [_i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _i64, _vp])
+_sig("qg_combine_rows_grad", _i32, [_i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                    _i64, _vp, _vp])
 
 
 def _check(rc, where):
@@ -408,6 +419,194 @@ def qconv2d_f32_dyn_a8w4(x, packed_w, Cout, KH, KW, stride, pad, bias, clamp_min
                                     float(clamp_max), 1 if symmetric else 0, _p(y), _p(q_out),
                                     _p(scale_out), _p(zp_out), _p(workspace), workspace.numel(),
                                     _stream(stream)), "qconv2d_f32_dyn_a8w4")
+
+
+# ---------------------------------------------------------------------------
+# Weight-only int4 products (bf16 rows), dense and per expert; expert order
+# ---------------------------------------------------------------------------
+W4_FORMATS = {"f32": 0, "bf16": 1, "asym": 2}  # qg_w4_format
+_DTYPES = {}                                   # torch dtype -> qg_dtype
+
+
+def _launch(fn, stream, tensors, args):
+    """Call fn(*args, stream) on the device that holds `tensors` (None entries
+    are skipped), on that device's current stream unless one is given."""
+    import torch
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn.__name__}: the tensors are not on one device")
+    if dev < 0:
+        raise ValueError(f"{fn.__name__}: expected CUDA tensors")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(stream))
+    elif stream is None:
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        rc = fn(*args, _stream(stream))
+    if rc != QG_OK:
+        raise QGError(rc, fn.__name__)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _row_dtype(*rows):
+    import torch
+    if not _DTYPES:
+        _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    code = _DTYPES.get(rows[0].dtype)
+    _need(code is not None, "rows are float32, bfloat16 or float16")
+    for r in rows:
+        _need(r.dtype == rows[0].dtype, "the rows have one dtype")
+        _need(r.dim() == 2 and (r.stride(1) == 1 or r.shape[1] == 1), "expected row-major 2-D rows")
+    return code
+
+
+def _row_ld(t):
+    """Row stride of a 2-D view; of a single row, at least its length."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _int32(t, shape, what):
+    import torch
+    _need(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape,
+          f"{what}: expected contiguous int32 {shape}")
+
+
+def _float32(t, shape, what):
+    import torch
+    if t is not None:
+        _need(t.dtype == torch.float32 and t.is_contiguous() and tuple(t.shape) == shape,
+              f"{what}: expected contiguous float32 {shape}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _w4_bytes(N, K, fmt):
+    return N * (K // 2) + N * (K // 32) * (4, 2, 8)[fmt]
+
+
+def _product_rows(x, y, packed_w, weights):
+    import torch
+    fmt = W4_FORMATS.get(weights)
+    _need(fmt is not None, f"weights: expected one of {sorted(W4_FORMATS)}")
+    _need(x.dtype == torch.bfloat16, "the rows are bfloat16")
+    _row_dtype(x, y)
+    _need(packed_w.dtype == torch.uint8, "packed_w: expected uint8")
+    return fmt
+
+
+def _experts_packed(packed_w, E, N, K, fmt):
+    """Bytes from one expert's packed matrix to the next."""
+    _need(packed_w.dim() == 2 and packed_w.shape[0] == E and packed_w.stride(1) == 1
+          and packed_w.shape[1] >= _w4_bytes(N, K, fmt),
+          "packed_w: expected uint8 [E][bytes] that hold a packed matrix each")
+    return max(packed_w.stride(0), packed_w.shape[1])
+
+
+def qgemm_a16w4_bf16(x, packed_w, y, bias=None, weights="f32", stream=None):
+    """y = x @ W^T + bias; x bf16 [M][K], y bf16 [M][N], W packed by pack_w4_g32
+    (weights="f32"), pack_w4_g32_bf16 ("bf16") or pack_w4_g32_asym ("asym")."""
+    fmt = _product_rows(x, y, packed_w, weights)
+    (M, K), N = x.shape, y.shape[1]
+    _need(y.shape[0] == M, "x and y have the same number of rows")
+    _need(packed_w.is_contiguous() and packed_w.numel() >= _w4_bytes(N, K, fmt),
+          "packed_w is smaller than a packed [N][K] matrix")
+    _float32(bias, (N,), "bias")
+    _launch(lib.qgemm_a16w4_bf16, stream, (x, packed_w, y, bias),
+            (M, N, K, x.data_ptr(), _row_ld(x), packed_w.data_ptr(), fmt, _addr(bias),
+             y.data_ptr(), _row_ld(y)))
+
+
+def qgemm_a16w4_bf16_experts(x, offsets, packed_w, y, src=None, topk=1, bias=None, weights="f32",
+                             stream=None):
+    """y[p] = W[e] @ x[src[p] // topk] + bias[e] (x[p] without src) for the rows
+    p of expert e, offsets[e] <= p < offsets[e+1]; packed_w uint8 [E][bytes]."""
+    fmt = _product_rows(x, y, packed_w, weights)
+    (S, N), K, E = y.shape, x.shape[1], packed_w.shape[0]
+    step = _experts_packed(packed_w, E, N, K, fmt)
+    _int32(offsets, (E + 1,), "offsets")
+    if src is not None:
+        _int32(src, (S,), "src")
+    _float32(bias, (E, N), "bias")
+    _launch(lib.qgemm_a16w4_bf16_experts, stream, (x, offsets, packed_w, y, src, bias),
+            (E, S, N, K, x.data_ptr(), _row_ld(x), x.shape[0], _addr(src), topk,
+             offsets.data_ptr(), packed_w.data_ptr(), step, fmt, _addr(bias), y.data_ptr(),
+             _row_ld(y)))
+
+
+def qg_sort_by_expert_workspace_bytes(T, topk, E):
+    return lib.qg_sort_by_expert_workspace_bytes(T, topk, E)
+
+
+def qg_sort_by_expert(ids, offsets, src, pos, workspace=None, stream=None):
+    """Stable order of the entries ids [T][topk] by expert: offsets [E+1],
+    src [T*topk] (entry at a sorted position), pos [T][topk] (-1: no expert)."""
+    import torch
+    T, topk = ids.shape
+    E = offsets.shape[0] - 1
+    _need(ids.dtype == torch.int32 and (ids.stride(1) == 1 or topk == 1), "ids: expected int32 rows")
+    _int32(offsets, (E + 1,), "offsets")
+    _int32(src, (T * topk,), "src")
+    _int32(pos, (T, topk), "pos")
+    need = lib.qg_sort_by_expert_workspace_bytes(T, topk, E)
+    if need and workspace is None:
+        workspace = _empty_bytes(need, ids.device)
+    _launch(lib.qg_sort_by_expert, stream, (ids, offsets, src, pos, workspace),
+            (T, topk, E, ids.data_ptr(), _row_ld(ids), offsets.data_ptr(), src.data_ptr(),
+             pos.data_ptr(), _addr(workspace),
+             0 if workspace is None else workspace.numel() * workspace.element_size()))
+
+
+def qg_spread_rows(x, pos, xs, stream=None):
+    """xs[pos[t, j]] = x[t]; negative positions are left out."""
+    dt = _row_dtype(x, xs)
+    T, N = x.shape
+    topk = pos.shape[1]
+    _int32(pos, (T, topk), "pos")
+    _need(xs.shape[1] == N, "x and xs have rows of one length")
+    _launch(lib.qg_spread_rows, stream, (x, pos, xs),
+            (T, topk, xs.shape[0], N, dt, x.data_ptr(), _row_ld(x), pos.data_ptr(),
+             xs.data_ptr(), _row_ld(xs)))
+
+
+def qg_combine_rows(ys, pos, y, weights=None, stream=None):
+    """y[t] = sum_j weights[t, j] * ys[pos[t, j]] (weights None: 1)."""
+    dt = _row_dtype(ys, y)
+    T, N = y.shape
+    topk = pos.shape[1]
+    _int32(pos, (T, topk), "pos")
+    _float32(weights, (T, topk), "weights")
+    _need(ys.shape[1] == N, "ys and y have rows of one length")
+    _launch(lib.qg_combine_rows, stream, (ys, pos, y, weights),
+            (T, topk, ys.shape[0], N, dt, ys.data_ptr(), _row_ld(ys), pos.data_ptr(),
+             _addr(weights), y.data_ptr(), _row_ld(y)))
+
+
+def qg_combine_rows_grad(dy, ys, pos, weights, dys, dw, stream=None):
+    """Gradients of qg_combine_rows: dys[pos[t, j]] = weights[t, j] * dy[t] and
+    dw[t, j] = <dy[t], ys[pos[t, j]]>.  dys or dw (then also ys) may be None."""
+    rows = [r for r in (dy, ys, dys) if r is not None]
+    dt = _row_dtype(*rows)
+    T, N = dy.shape
+    topk = pos.shape[1]
+    _int32(pos, (T, topk), "pos")
+    _float32(weights, (T, topk), "weights")
+    _float32(dw, (T, topk), "dw")
+    _need(dw is None or ys is not None, "dw needs ys")
+    _need(all(r.shape[1] == N for r in rows), "dy, ys and dys have rows of one length")
+    S = (ys if ys is not None else dys if dys is not None else dy).shape[0]
+    _need(ys is None or dys is None or ys.shape[0] == dys.shape[0], "ys and dys have the same rows")
+    _launch(lib.qg_combine_rows_grad, stream, (dy, ys, pos, weights, dys, dw),
+            (T, topk, S, N, dt, dy.data_ptr(), _row_ld(dy), _addr(ys),
+             N if ys is None else _row_ld(ys), pos.data_ptr(), _addr(weights), _addr(dys),
+             N if dys is None else _row_ld(dys), _addr(dw)))
 
 
 def exported_symbols():

@@ -38,6 +38,8 @@ int setup_a8w4_gemv();
 int setup_a8w4_gemm_simt();
 int i8gemm_setup();
 int a8w4_tc_setup();
+int a16w4_setup();
+int expert_rows_setup();
 
 int i8gemm_pack_b(int K, int N, const int8_t* B, int64_t ldb, void* packed, cudaStream_t st);
 size_t i8gemm_pack_b_bytes(int K, int N);
@@ -90,6 +92,8 @@ DeviceState* current_state() {
       if (rc == QG_OK) rc = setup_a8w4_gemm_simt();
       if (rc == QG_OK) rc = i8gemm_setup();
       if (rc == QG_OK) rc = a8w4_tc_setup();
+      if (rc == QG_OK) rc = a16w4_setup();
+      if (rc == QG_OK) rc = expert_rows_setup();
       s.setup_rc = rc;
     }
     s.ready = true;

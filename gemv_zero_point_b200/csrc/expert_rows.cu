@@ -1,0 +1,577 @@
+// Tokens in the order of their experts, and back: the stable order by expert
+// id, token rows spread to their sorted positions, the weighted sum of the
+// sorted rows per token, and the gradients of both.
+//
+//   order    sorted position p of entry i = t*topk + j with expert id e:
+//            p = #{entries of smaller ids} + #{entries of id e before i}
+//   spread   xs[pos[t,j]] = x[t]            (gradient: the sum below, weights 1)
+//   combine  y[t] = sum_j w[t,j] * ys[pos[t,j]]
+//   its gradient  dys[pos[t,j]] = w[t,j] * dy[t],  dw[t,j] = <dy[t], ys[pos[t,j]]>
+//
+// The row kernels are bound by HBM: each moves every row it needs once, in
+// 16-byte accesses where the rows allow it.  Walking the tokens (not the
+// sorted rows) lets a token's row be read once for its topk copies, and lets
+// combine's gradient read dy once for all of a token's experts.  Sums are
+// held in f32 and rounded once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <stdint.h>
+
+#include "qg_internal.cuh"
+
+namespace qg {
+
+int device_setup_status();
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Order by expert
+// ---------------------------------------------------------------------------
+// A warp owns a contiguous run of entries and takes it 32 at a time:
+// __match_any_sync groups the lanes of one expert, the lanes below a lane in
+// its group give its rank, and the warp's own counters in shared memory carry
+// the rank from one 32 to the next.  No atomics, so the order is the stable
+// one by construction.
+constexpr int kSortMaxE = 1024;
+constexpr int kSortOneWarps = 32;        // one CTA sorts everything
+constexpr int64_t kSortOneMax = 16384;   // most entries of the one-CTA form
+constexpr int64_t kSortMax = 1 << 22;    // each CTA reads every chunk's counts
+constexpr int kSortWarps = 16;           // several CTAs
+constexpr int kSortChunk = 4096;         // entries per CTA then
+
+__device__ __forceinline__ int expert_of(const int32_t* ids, int64_t ld, int topk, int64_t i,
+                                         int64_t n, int E) {
+  if (i >= n) return -1;
+  const int64_t t = i / topk;
+  const int e = ids[t * ld + (i - t * topk)];
+  return (unsigned)e < (unsigned)E ? e : -1;
+}
+
+// Adds this warp's run [i0, i1) to its counters cnt[E] (zeroed before).
+__device__ __forceinline__ void count_run(const int32_t* ids, int64_t ld, int topk, int64_t i0,
+                                          int64_t i1, int E, int* cnt) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t b = i0; b < i1; b += 32) {
+    const int e = expert_of(ids, ld, topk, b + lane, i1, E);
+    const uint32_t m = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && lane == __ffs(m) - 1) cnt[e] += __popc(m);
+    __syncwarp();
+  }
+}
+
+// Places this warp's run: next[e] is the sorted position of its next entry of e.
+__device__ __forceinline__ void place_run(const int32_t* ids, int64_t ld, int topk, int64_t i0,
+                                          int64_t i1, int E, int* next, int32_t* src,
+                                          int32_t* pos) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t b = i0; b < i1; b += 32) {
+    const int64_t i = b + lane;
+    const int e = expert_of(ids, ld, topk, i, i1, E);
+    const uint32_t m = __match_any_sync(0xffffffffu, e);
+    int p = -1;
+    if (e >= 0) p = next[e] + __popc(m & ((1u << lane) - 1u));
+    __syncwarp();
+    if (e >= 0 && lane == __ffs(m) - 1) next[e] += __popc(m);
+    __syncwarp();
+    if (i < i1) {
+      pos[i] = p;
+      if (p >= 0) src[p] = (int32_t)i;
+    }
+  }
+}
+
+// Exclusive prefix sum over v[0, E) in place by the whole CTA; v[E] = total.
+__device__ __forceinline__ void scan_experts(int* v, int E, int* part /* [33] */) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int carry = 0;
+  for (int b = 0; b < E; b += blockDim.x) {
+    const int i = b + threadIdx.x;
+    const int own = i < E ? v[i] : 0;
+    int x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    int before = carry, total = 0;
+    for (int w = 0; w < nw; ++w) {
+      const int s = part[w];
+      if (w < warp) before += s;
+      total += s;
+    }
+    if (i < E) v[i] = before + x - own;
+    carry += total;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) v[E] = carry;
+  __syncthreads();
+}
+
+// Dynamic shared memory: base[E + 1], then cnt[warps][E].
+// hist == NULL: one CTA holds every entry.  Otherwise hist[chunks][E] holds
+// each chunk's counts and this CTA places chunk blockIdx.x.
+__global__ void __launch_bounds__(kSortOneWarps * 32)
+    sort_place_kernel(int64_t n, int topk, int E, const int32_t* __restrict__ ids, int64_t ld,
+                      const int32_t* __restrict__ hist, int64_t per_cta,
+                      int32_t* __restrict__ offsets, int32_t* __restrict__ src,
+                      int32_t* __restrict__ pos) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ int sort_smem[];
+  __shared__ int part[33];
+  int* base = sort_smem;
+  int* cnt = sort_smem + E + 1;
+  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  for (int i = threadIdx.x; i < nw * E; i += blockDim.x) cnt[i] = 0;
+  const int64_t c0 = (int64_t)blockIdx.x * per_cta;
+  const int64_t c1 = min64(n, c0 + per_cta);
+  const int64_t run = ((c1 - c0 + nw * 32 - 1) / (nw * 32)) * 32;  // entries per warp
+  const int64_t i0 = min64(c1, c0 + warp * run), i1 = min64(c1, i0 + run);
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  count_run(ids, ld, topk, i0, i1, E, cnt + warp * E);
+  __syncthreads();
+  // base[e]: entries of e in all chunks; the earlier chunks' part is added
+  // to the warps' starts below
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int all = 0, before = 0;
+    if (hist) {
+      for (int c = 0; c < (int)gridDim.x; ++c) {
+        const int h = hist[(int64_t)c * E + e];
+        all += h;
+        if (c < (int)blockIdx.x) before += h;
+      }
+    }
+    int here = before;
+    for (int w = 0; w < nw; ++w) {
+      const int k = cnt[w * E + e];
+      cnt[w * E + e] = here;
+      here += k;
+    }
+    base[e] = hist ? all : here;
+  }
+  __syncthreads();
+  scan_experts(base, E, part);
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = base[e];
+  for (int i = threadIdx.x; i < nw * E; i += blockDim.x) cnt[i] += base[i % E];
+  __syncthreads();
+  place_run(ids, ld, topk, i0, i1, E, cnt + warp * E, src, pos);
+}
+
+// Counts of each chunk, for the form with several CTAs.
+__global__ void __launch_bounds__(kSortWarps * 32)
+    sort_count_kernel(int64_t n, int topk, int E, const int32_t* __restrict__ ids, int64_t ld,
+                      int32_t* __restrict__ hist) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ int sort_smem[];
+  for (int i = threadIdx.x; i < E; i += blockDim.x) sort_smem[i] = 0;
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t c0 = (int64_t)blockIdx.x * kSortChunk, c1 = min64(n, c0 + kSortChunk);
+  for (int64_t i = c0 + threadIdx.x; i < c1; i += blockDim.x) {
+    const int e = expert_of(ids, ld, topk, i, c1, E);
+    if (e >= 0) atomicAdd(&sort_smem[e], 1);  // integers: any order gives the same count
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x)
+    hist[(int64_t)blockIdx.x * E + e] = sort_smem[e];
+}
+
+// ---------------------------------------------------------------------------
+// Rows
+// ---------------------------------------------------------------------------
+// V values of type T as one access of V * sizeof(T) bytes.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T v[V];
+};
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// Sorted position of (t, j), or -1 when the entry has no expert.  A position
+// outside [0, S) is an error of the caller's: recorded, then treated as -1.
+__device__ __forceinline__ int64_t place_of(const int32_t* pos, int64_t i, int64_t S, int* status) {
+  const int p = __ldg(pos + i);
+  if (p >= S) {
+    record_error(status, QG_ERR_INVALID_ARG);
+    return -1;
+  }
+  return p < 0 ? -1 : p;
+}
+
+constexpr int JB = 8;  // experts of a token taken together
+
+template <typename W>
+__global__ void __launch_bounds__(256)
+    spread_rows_kernel(int topk, int64_t S, int64_t nv, const W* __restrict__ x,
+                                   int64_t ldx, const int32_t* __restrict__ pos,
+                                   W* __restrict__ xs, int64_t ldxs, int* status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t t = blockIdx.x;
+  const W* xr = x + t * ldx;
+  const int64_t i0 = (int64_t)blockIdx.y * blockDim.x * 2 + threadIdx.x;
+  const int64_t step = (int64_t)gridDim.y * blockDim.x * 2;
+  for (int jb = 0; jb < topk; jb += JB) {
+    int64_t p[JB];
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+      p[j] = jb + j < topk ? place_of(pos, t * topk + jb + j, S, status) : -1;
+    for (int64_t i = i0; i < nv; i += step) {
+      const int64_t i2 = i + blockDim.x;
+      const W a = xr[i];
+      W b = a;
+      if (i2 < nv) b = xr[i2];
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        if (p[j] < 0) continue;
+        W* d = xs + p[j] * ldxs;
+        d[i] = a;
+        if (i2 < nv) d[i2] = b;
+      }
+    }
+  }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(256)
+    combine_rows_kernel(int topk, int64_t S, int64_t nv, const T* __restrict__ ys,
+                                    int64_t ldys, const int32_t* __restrict__ pos,
+                                    const float* __restrict__ w, T* __restrict__ y, int64_t ldy,
+                                    int* status) {
+  using P = Pack<T, V>;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t t = blockIdx.x;
+  const int64_t step = (int64_t)gridDim.y * blockDim.x;
+  for (int64_t i = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; i < nv; i += step) {
+    float acc[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+    for (int jb = 0; jb < topk; jb += JB) {
+      P r[JB];
+      float wj[JB];
+      bool live[JB];
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        const int64_t p = jb + j < topk ? place_of(pos, t * topk + jb + j, S, status) : -1;
+        live[j] = p >= 0;
+        wj[j] = 1.0f;
+        if (live[j]) {
+          r[j] = reinterpret_cast<const P*>(ys + p * ldys)[i];
+          if (w) wj[j] = __ldg(w + t * topk + jb + j);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        if (!live[j]) continue;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(wj[j], to_f32(r[j].v[k]), acc[k]);
+      }
+    }
+    P out;
+#pragma unroll
+    for (int k = 0; k < V; ++k) out.v[k] = from_f32<T>(acc[k]);
+    reinterpret_cast<P*>(y + t * ldy)[i] = out;
+  }
+}
+
+// One CTA per token: the dot products of its experts' rows with dy[t] need
+// the whole row, and dy is read once for JB of them.
+template <typename T, int V>
+__global__ void __launch_bounds__(512)
+    combine_grad_kernel(int topk, int64_t S, int64_t nv, const T* __restrict__ dy,
+                                    int64_t lddy, const T* __restrict__ ys, int64_t ldys,
+                                    const int32_t* __restrict__ pos, const float* __restrict__ w,
+                                    T* __restrict__ dys, int64_t lddys, float* __restrict__ dw,
+                                    int* status) {
+  using P = Pack<T, V>;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float red[JB][32];
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  for (int jb = 0; jb < topk; jb += JB) {
+    int64_t p[JB];
+    float wj[JB], dot[JB];
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+      p[j] = jb + j < topk ? place_of(pos, t * topk + jb + j, S, status) : -1;
+      wj[j] = (w && p[j] >= 0) ? __ldg(w + t * topk + jb + j) : 1.0f;
+      dot[j] = 0.0f;
+    }
+    for (int64_t i = threadIdx.x; i < nv; i += blockDim.x) {
+      const P g = reinterpret_cast<const P*>(dy + t * lddy)[i];
+      P r[JB];
+      if (dw) {
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+          if (p[j] >= 0) r[j] = reinterpret_cast<const P*>(ys + p[j] * ldys)[i];
+      }
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        if (p[j] < 0) continue;
+        if (dw) {
+#pragma unroll
+          for (int k = 0; k < V; ++k) dot[j] = fmaf(to_f32(g.v[k]), to_f32(r[j].v[k]), dot[j]);
+        }
+        if (dys) {
+          P out;
+#pragma unroll
+          for (int k = 0; k < V; ++k) out.v[k] = from_f32<T>(wj[j] * to_f32(g.v[k]));
+          reinterpret_cast<P*>(dys + p[j] * lddys)[i] = out;
+        }
+      }
+    }
+    if (dw) {
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+        if (lane == 0) red[j][warp] = dot[j];
+      }
+      __syncthreads();
+      if (threadIdx.x < JB && jb + (int)threadIdx.x < topk) {
+        float s = 0.0f;
+        for (int k = 0; k < nw; ++k) s += red[threadIdx.x][k];
+        dw[t * topk + jb + threadIdx.x] = s;  // 0 for an entry without an expert
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+// Programmatic dependents of the work before them: they may become resident
+// while it drains and wait for it on the device.
+template <typename F, typename... A>
+int launch_pdl(F kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+}
+
+int elem_bytes(int dtype) {
+  return dtype == QG_F32 ? 4 : (dtype == QG_BF16 || dtype == QG_F16) ? 2 : 0;
+}
+
+bool all_aligned(uintptr_t bits, int a) { return (bits & (uintptr_t)(a - 1)) == 0; }
+
+// Threads of a row of nv accesses: enough to cover it, at most `most`.
+int row_threads(int64_t nv, int most) {
+  return (int)min64(most, max64(32, round_up(nv, 32)));
+}
+
+template <typename T>
+int run_combine(int vec, int T_, int topk, int64_t S, int N, const void* ys, int64_t ldys,
+                const int32_t* pos, const float* w, void* y, int64_t ldy, cudaStream_t st) {
+  const int64_t nv = N / vec;
+  const int th = row_threads(nv, 256);
+  // a few tokens: several CTAs share a token's row
+  const int parts = (int)max64(1, min64(cdiv(nv, th), cdiv(2 * num_sms(), T_)));
+  const dim3 grid((unsigned)T_, (unsigned)parts);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, th, 0, st, topk, S, nv, (const T*)ys, ldys, pos, w, (T*)y,
+                      ldy, status_word());
+  };
+  if (vec * sizeof(T) == 16) return go(combine_rows_kernel<T, 16 / sizeof(T)>);
+  if (vec * sizeof(T) == 4 && sizeof(T) == 2) return go(combine_rows_kernel<T, 4 / sizeof(T)>);
+  return go(combine_rows_kernel<T, 1>);
+}
+
+template <typename T>
+int run_combine_grad(int vec, int T_, int topk, int64_t S, int N, const void* dy, int64_t lddy,
+                     const void* ys, int64_t ldys, const int32_t* pos, const float* w, void* dys,
+                     int64_t lddys, float* dw, cudaStream_t st) {
+  const int64_t nv = N / vec;
+  const int th = row_threads(nv, T_ >= 8 * num_sms() ? 128 : 512);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3((unsigned)T_), th, 0, st, topk, S, nv, (const T*)dy, lddy,
+                      (const T*)ys, ldys, pos, w, (T*)dys, lddys, dw, status_word());
+  };
+  if (vec * sizeof(T) == 16) return go(combine_grad_kernel<T, 16 / sizeof(T)>);
+  if (vec * sizeof(T) == 4 && sizeof(T) == 2) return go(combine_grad_kernel<T, 4 / sizeof(T)>);
+  return go(combine_grad_kernel<T, 1>);
+}
+
+// Values per access that every pointer, stride and the row length allow.
+int vector_of(int esz, uintptr_t bits) {
+  if (all_aligned(bits, 16)) return 16 / esz;
+  if (esz == 2 && all_aligned(bits, 4)) return 2;
+  return 1;
+}
+
+// Sizes common to the row entry points: QG_OK, or what the call returns.
+int row_args(int T, int topk, int S, int N, int dtype) {
+  if (T < 0 || topk <= 0 || S < 0 || N <= 0) return QG_ERR_INVALID_ARG;
+  if (!elem_bytes(dtype)) return QG_ERR_INVALID_ARG;
+  if ((int64_t)T * topk > INT32_MAX) return QG_ERR_UNSUPPORTED;
+  return QG_OK;
+}
+
+}  // namespace
+
+int expert_rows_setup() {
+  const int most = (kSortOneWarps * kSortMaxE + kSortMaxE + 1) * 4;
+  return cudaFuncSetAttribute((const void*)sort_place_kernel,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              most) == cudaSuccess
+             ? QG_OK
+             : QG_ERR_CUDA;
+}
+
+}  // namespace qg
+
+using namespace qg;
+
+// ---------------------------------------------------------------------------
+// Entry points
+// ---------------------------------------------------------------------------
+extern "C" size_t qg_sort_by_expert_workspace_bytes(int T, int topk, int E) {
+  if (T <= 0 || topk <= 0 || E <= 0 || E > kSortMaxE) return 0;
+  const int64_t n = (int64_t)T * topk;
+  if (n > kSortMax || n <= kSortOneMax) return 0;
+  return (size_t)(cdiv(n, kSortChunk) * E * 4);
+}
+
+extern "C" int qg_sort_by_expert(int T, int topk, int E, const int32_t* ids, int64_t ld_ids,
+                                 int32_t* offsets, int32_t* src, int32_t* pos, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (T < 0 || topk <= 0 || E <= 0 || ld_ids < topk) return QG_ERR_INVALID_ARG;
+  if (E > kSortMaxE || (int64_t)T * topk > kSortMax) return QG_ERR_UNSUPPORTED;
+  if (!offsets || (T > 0 && (!ids || !src || !pos))) return QG_ERR_INVALID_ARG;
+  if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)src | (uintptr_t)pos) & 3)
+    return QG_ERR_MISALIGNED;
+  const size_t need = qg_sort_by_expert_workspace_bytes(T, topk, E);
+  if (need && (!workspace || workspace_bytes < need)) return QG_ERR_WORKSPACE;
+  if (need && ((uintptr_t)workspace & 3)) return QG_ERR_MISALIGNED;
+  const int rc = device_setup_status();
+  if (rc != QG_OK) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int64_t n = (int64_t)T * topk;
+  if (!need) {
+    // one CTA; fewer warps for few entries (each costs E counters to clear)
+    const int warps = (int)min64(kSortOneWarps, max64(8, cdiv(n, 64)));
+    return launch_pdl(sort_place_kernel, dim3(1), warps * 32,
+                      (size_t)(warps * E + E + 1) * 4, st, n, topk, E, ids, ld_ids,
+                      (const int32_t*)nullptr, n, offsets, src, pos);
+  }
+  const unsigned chunks = (unsigned)cdiv(n, kSortChunk);
+  const int rc2 = launch_pdl(sort_count_kernel, dim3(chunks), kSortWarps * 32, (size_t)E * 4, st,
+                             n, topk, E, ids, ld_ids, (int32_t*)workspace);
+  if (rc2 != QG_OK) return rc2;
+  return launch_pdl(sort_place_kernel, dim3(chunks), kSortWarps * 32,
+                    (size_t)(kSortWarps * E + E + 1) * 4, st, n, topk, E, ids, ld_ids,
+                    (const int32_t*)workspace, (int64_t)kSortChunk, offsets, src, pos);
+}
+
+extern "C" int qg_spread_rows(int T, int topk, int S, int N, int dtype, const void* x,
+                              int64_t ldx, const int32_t* pos, void* xs, int64_t ldxs,
+                              void* stream) {
+  int rc = row_args(T, topk, S, N, dtype);
+  if (rc != QG_OK) return rc;
+  if (ldx < N || ldxs < N) return QG_ERR_INVALID_ARG;
+  if (T == 0 || S == 0) return QG_OK;
+  if (!x || !pos || !xs) return QG_ERR_INVALID_ARG;
+  const int esz = elem_bytes(dtype);
+  if (((uintptr_t)x | (uintptr_t)xs) % esz || ((uintptr_t)pos & 3)) return QG_ERR_MISALIGNED;
+  rc = device_setup_status();
+  if (rc != QG_OK) return rc;
+  const int64_t rb = (int64_t)N * esz, xb = ldx * esz, sb = ldxs * esz;
+  const uintptr_t bits = (uintptr_t)x | (uintptr_t)xs | (uintptr_t)rb | (uintptr_t)xb | (uintptr_t)sb;
+  cudaStream_t st = (cudaStream_t)stream;
+  auto go = [&](auto kernel, auto* word) {
+    using W = std::remove_pointer_t<decltype(word)>;
+    const int64_t nv = rb / (int64_t)sizeof(W);
+    const int th = row_threads(cdiv(nv, 2), 256);
+    // a few tokens: several CTAs share a token's row
+    const int parts = (int)max64(1, min64(cdiv(nv, 2 * th), cdiv(2 * num_sms(), T)));
+    return launch_pdl(kernel, dim3((unsigned)T, (unsigned)parts), th, 0, st, topk, (int64_t)S, nv,
+                      (const W*)x, xb / (int64_t)sizeof(W), pos, (W*)xs, sb / (int64_t)sizeof(W),
+                      status_word());
+  };
+  if (all_aligned(bits, 16)) return go(spread_rows_kernel<uint4>, (uint4*)nullptr);
+  if (all_aligned(bits, 4)) return go(spread_rows_kernel<uint32_t>, (uint32_t*)nullptr);
+  return go(spread_rows_kernel<uint16_t>, (uint16_t*)nullptr);
+}
+
+extern "C" int qg_combine_rows(int T, int topk, int S, int N, int dtype, const void* ys,
+                               int64_t ldys, const int32_t* pos, const float* weights, void* y,
+                               int64_t ldy, void* stream) {
+  int rc = row_args(T, topk, S, N, dtype);
+  if (rc != QG_OK) return rc;
+  if (ldys < N || ldy < N) return QG_ERR_INVALID_ARG;
+  if (T == 0) return QG_OK;
+  if (!pos || !y || (S > 0 && !ys)) return QG_ERR_INVALID_ARG;
+  const int esz = elem_bytes(dtype);
+  if (((uintptr_t)ys | (uintptr_t)y) % esz || (((uintptr_t)pos | (uintptr_t)weights) & 3))
+    return QG_ERR_MISALIGNED;
+  rc = device_setup_status();
+  if (rc != QG_OK) return rc;
+  const uintptr_t bits = (uintptr_t)ys | (uintptr_t)y | (uintptr_t)((int64_t)N * esz) |
+                         (uintptr_t)(ldys * esz) | (uintptr_t)(ldy * esz);
+  const int vec = vector_of(esz, bits);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == QG_F32)
+    return run_combine<float>(vec, T, topk, S, N, ys, ldys, pos, weights, y, ldy, st);
+  if (dtype == QG_F16)
+    return run_combine<__half>(vec, T, topk, S, N, ys, ldys, pos, weights, y, ldy, st);
+  return run_combine<__nv_bfloat16>(vec, T, topk, S, N, ys, ldys, pos, weights, y, ldy, st);
+}
+
+extern "C" int qg_combine_rows_grad(int T, int topk, int S, int N, int dtype, const void* dy,
+                                    int64_t lddy, const void* ys, int64_t ldys,
+                                    const int32_t* pos, const float* weights, void* dys,
+                                    int64_t lddys, float* dw, void* stream) {
+  int rc = row_args(T, topk, S, N, dtype);
+  if (rc != QG_OK) return rc;
+  if (lddy < N || (dw && ldys < N) || (dys && lddys < N)) return QG_ERR_INVALID_ARG;
+  if (!dys && !dw) return QG_ERR_INVALID_ARG;
+  if (T == 0) return QG_OK;
+  if (!dy || !pos || (dw && S > 0 && !ys)) return QG_ERR_INVALID_ARG;
+  const int esz = elem_bytes(dtype);
+  if (((uintptr_t)dy | (uintptr_t)(dw ? ys : nullptr) | (uintptr_t)dys) % esz ||
+      (((uintptr_t)pos | (uintptr_t)weights | (uintptr_t)dw) & 3))
+    return QG_ERR_MISALIGNED;
+  rc = device_setup_status();
+  if (rc != QG_OK) return rc;
+  uintptr_t bits = (uintptr_t)dy | (uintptr_t)((int64_t)N * esz) | (uintptr_t)(lddy * esz);
+  if (dw) bits |= (uintptr_t)ys | (uintptr_t)(ldys * esz);
+  if (dys) bits |= (uintptr_t)dys | (uintptr_t)(lddys * esz);
+  const int vec = vector_of(esz, bits);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == QG_F32)
+    return run_combine_grad<float>(vec, T, topk, S, N, dy, lddy, ys, ldys, pos, weights, dys,
+                                   lddys, dw, st);
+  if (dtype == QG_F16)
+    return run_combine_grad<__half>(vec, T, topk, S, N, dy, lddy, ys, ldys, pos, weights, dys,
+                                    lddys, dw, st);
+  return run_combine_grad<__nv_bfloat16>(vec, T, topk, S, N, dy, lddy, ys, ldys, pos, weights,
+                                         dys, lddys, dw, st);
+}

@@ -413,6 +413,99 @@ int qconv2d_f32_dyn_a8w4(int Nb, int H, int W, int Cin, int Cout, int KH, int KW
                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Weight-only int4 linear: bf16 rows, not quantized, times the int4 weights
+ * of pack_w4_g32 / pack_w4_g32_bf16 / pack_w4_g32_asym (the packings above,
+ * so one packed matrix serves the A8W4 calls and these).  The pages have no
+ * counterpart for bf16 activations.
+ *   y[m,n] = sum_k x[m,k] * w[n,k] + bias[n]
+ *   w[n,k] = sw[n,g] * c[n,k] (+ zw[n,g]),  g = k/32, c the int4 code
+ *   x: bf16 [M][ldx] (ldx >= K), 16-byte aligned, ldx % 8 == 0
+ *   packed_w: 16-byte aligned, in the packing that `format` names (qg_w4_format)
+ *   bias: f32 [N] or NULL;  y: bf16 [M][ldy] (ldy >= N), any alignment
+ * K % 64 == 0 (else QG_ERR_UNSUPPORTED); M >= 0, any N >= 1.  No workspace.
+ * Sums are held in f32 and y is rounded once.  Rows of x do not mix: a
+ * non-finite value in one row reaches that row of y alone.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  QG_W4_F32 = 0,  /* pack_w4_g32: f32 group scales */
+  QG_W4_BF16 = 1, /* pack_w4_g32_bf16: bf16 group scales */
+  QG_W4_ASYM = 2  /* pack_w4_g32_asym: f32 group scales and f32 zeros */
+} qg_w4_format;
+
+int qgemm_a16w4_bf16(int M, int N, int K, const void* x, int64_t ldx, const void* packed_w,
+                     int format, const float* bias, void* y, int64_t ldy, void* stream);
+
+/*
+ * The same product per expert, for rows in the order of their experts
+ * (qg_sort_by_expert): rows [offsets[e], offsets[e+1]) of y are expert e's,
+ *   y[p] = W[e] @ x[r] + bias[e],  r = src[p] / topk, or r = p when src is NULL.
+ *   offsets: device int32 [E + 1], 0 <= offsets[e] <= offsets[e+1] <= S
+ *   src: device int32 [S] or NULL;  x: bf16 [x_rows][ldx], as above
+ *   packed_w: E packed matrices, the next one expert_bytes further (at least
+ *   the pack's size, a multiple of 16);  bias: f32 [E][N] or NULL
+ *   y: bf16 [S][ldy].  Rows that belong to no expert (before offsets[0],
+ *   from offsets[E] on) are left as they are.
+ * E <= 1024, K % 64 == 0 (else QG_ERR_UNSUPPORTED).  Nothing is read back to
+ * the host.  An expert whose range is not inside [0, S) gets no rows, and a
+ * src entry that reaches outside x counts as a row of zeros; both record
+ * QG_ERR_INVALID_ARG in the device status.
+ */
+int qgemm_a16w4_bf16_experts(int E, int S, int N, int K, const void* x, int64_t ldx, int x_rows,
+                             const int32_t* src, int topk, const int32_t* offsets,
+                             const void* packed_w, int64_t expert_bytes, int format,
+                             const float* bias, void* y, int64_t ldy, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Tokens in the order of their experts, and back.  The pages have no
+ * counterpart.  A token t has topk entries i = t*topk + j, each with an expert
+ * id; an id outside [0, E) means that the entry has no expert (a padding
+ * token, an expert of another rank).
+ *
+ * qg_sort_by_expert: the stable order by expert.
+ *   ids: int32 [T][ld_ids] (ld_ids >= topk).
+ *   offsets: int32 [E + 1], offsets[e] entries have an id below e.
+ *   pos: int32 [T][topk], the sorted position of entry (t, j), -1 if it has
+ *   no expert.  src: int32 [T*topk], the entry at a sorted position (the
+ *   inverse of pos); places from offsets[E] on are left as they are.
+ *   Entries of one expert keep their order.  E <= 1024, T*topk <= 4194304
+ *   (else QG_ERR_UNSUPPORTED).  Workspace: qg_sort_by_expert_workspace_bytes
+ *   (0: none), 4-byte aligned.
+ * ------------------------------------------------------------------------ */
+size_t qg_sort_by_expert_workspace_bytes(int T, int topk, int E);
+int qg_sort_by_expert(int T, int topk, int E, const int32_t* ids, int64_t ld_ids,
+                      int32_t* offsets, int32_t* src, int32_t* pos, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * Rows to their sorted positions and back.  dtype (qg_dtype) is the type of
+ * the rows; pos int32 [T][topk] as above: distinct places in [0, S), or
+ * negative for none (a place from S on is not touched and records
+ * QG_ERR_INVALID_ARG in the device status).  Row strides may have any
+ * alignment of the element; rows whose pointers, strides and lengths are
+ * multiples of 16 bytes move fastest.
+ *   qg_spread_rows:       xs[pos[t,j]] = x[t]; x [T][ldx], xs [S][ldxs].  Rows of
+ *                         xs that are no entry's place are left as they are.
+ *                         Its gradient is qg_combine_rows with weights NULL.
+ *   qg_combine_rows:      y[t] = sum_j weights[t,j] * ys[pos[t,j]], entries
+ *                         without a place left out (all of them: zeros);
+ *                         weights f32 [T][topk], or NULL for 1.
+ *   qg_combine_rows_grad: dys[pos[t,j]] = weights[t,j] * dy[t] and
+ *                         dw[t,j] = sum_n dy[t,n] * ys[pos[t,j],n] (0 without a
+ *                         place); dys or dw may be NULL (ys is not read then).
+ * Sums are held in f32 in a fixed order and rounded once.
+ */
+typedef enum { QG_F32 = 0, QG_BF16 = 1, QG_F16 = 2 } qg_dtype;
+
+int qg_spread_rows(int T, int topk, int S, int N, int dtype, const void* x, int64_t ldx,
+                   const int32_t* pos, void* xs, int64_t ldxs, void* stream);
+int qg_combine_rows(int T, int topk, int S, int N, int dtype, const void* ys, int64_t ldys,
+                    const int32_t* pos, const float* weights, void* y, int64_t ldy,
+                    void* stream);
+int qg_combine_rows_grad(int T, int topk, int S, int N, int dtype, const void* dy, int64_t lddy,
+                         const void* ys, int64_t ldys, const int32_t* pos, const float* weights,
+                         void* dys, int64_t lddys, float* dw, void* stream);
+
+/* ------------------------------------------------------------------------
  * qgemm_a8w4_f32 without a workspace.  The pages have no counterpart: this
  * entry point exists for callers that cannot allocate device memory for
  * scratch — a plugin inside a host framework that owns the allocator and

@@ -672,3 +672,47 @@ def qconv2d_f32_dyn_a8w4(x, qw, sw, stride, pad, bias, clamp_min, clamp_max,
     y = a8w4_from_codes(qA, sA, za, qw.reshape(Cout, KH * KW * Cin), sw, bias,
                         clamp_min, clamp_max)
     return y.reshape(Nb, OH, OW, Cout), qA, sA, za
+
+
+# ---------------------------------------------------------------------------
+# Weight-only int4 products and the expert order of tokens (no page shows
+# them; defined here by their formulas)
+# ---------------------------------------------------------------------------
+def w4_values(qw, sw, zw=None):
+    """The real weights sw*code (+ zw), float64: [..., N, K] from group values
+    [..., N, K/32]."""
+    qw = np.asarray(qw)
+    w = qw.astype(np.float64) * np.repeat(np.asarray(sw, np.float64), GROUP, axis=-1)
+    return w if zw is None else w + np.repeat(np.asarray(zw, np.float64), GROUP, axis=-1)
+
+
+def a16w4(x, w, bias=None):
+    """y = x @ w^T + bias in float64."""
+    y = np.asarray(x, np.float64) @ np.asarray(w, np.float64).T
+    return y if bias is None else y + np.asarray(bias, np.float64)
+
+
+def sort_by_expert(ids, E):
+    """Stable order of the entries of ids [T][topk] by expert id; ids outside
+    [0, E) have no expert.  Returns offsets [E+1], src (the entries in order)
+    and pos [T][topk] (-1: no expert)."""
+    flat = [int(i) for i in np.asarray(ids).reshape(-1)]
+    src, offsets = [], [0]
+    for e in range(E):
+        src += [i for i, v in enumerate(flat) if v == e]
+        offsets.append(len(src))
+    pos = np.full(len(flat), -1, np.int64)
+    for p, i in enumerate(src):
+        pos[i] = p
+    return np.array(offsets, np.int64), np.array(src, np.int64), pos.reshape(np.asarray(ids).shape)
+
+
+def combine_rows(ys, pos, weights, N):
+    """y[t] = sum_j weights[t,j] * ys[pos[t,j]] over the places >= 0, float64."""
+    T, topk = pos.shape
+    y = np.zeros((T, N))
+    for t in range(T):
+        for j in range(topk):
+            if pos[t, j] >= 0:
+                y[t] += (1.0 if weights is None else float(weights[t, j])) * ys[pos[t, j]].astype(np.float64)
+    return y
