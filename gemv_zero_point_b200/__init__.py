@@ -13,6 +13,7 @@ The function names are those of the C ABI:
   qconv2d_s8_im2col, qg_requant_params, qg_device_status,
   quantize_rows_a8_sym, qconv2d_f32_dyn_a8w4,
   qgemm_a16w4_bf16, qgemm_a16w4_bf16_experts,
+  qgemm_a16w4_bf16_grad_x, qgemm_a16w4_bf16_experts_grad_x,
   qg_sort_by_expert, qg_spread_rows, qg_combine_rows, qg_combine_rows_grad
 plus the *_bytes / *_workspace_bytes size queries.
 """
@@ -113,6 +114,9 @@ _sig("qgemm_a8w4_f32_bf16s", _i32, [_i32, _i32, _i32, _vp, _i64, _vp, _vp, _f32,
 _sig("qgemm_a16w4_bf16", _i32, [_i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _vp])
 _sig("qgemm_a16w4_bf16_experts", _i32, [_i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _vp,
                                         _i64, _i32, _vp, _vp, _i64, _vp])
+_sig("qgemm_a16w4_bf16_grad_x", _i32, [_i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _vp])
+_sig("qgemm_a16w4_bf16_experts_grad_x", _i32, [_i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i64,
+                                               _i32, _vp, _i64, _vp])
 _sig("qg_sort_by_expert_workspace_bytes", _sz, [_i32, _i32, _i32])
 _sig("qg_sort_by_expert", _i32, [_i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp])
 _sig("qg_spread_rows", _i32, [_i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp])
@@ -425,120 +429,159 @@ def qconv2d_f32_dyn_a8w4(x, packed_w, Cout, KH, KW, stride, pad, bias, clamp_min
 # Weight-only int4 products (bf16 rows), dense and per expert; expert order
 # ---------------------------------------------------------------------------
 W4_FORMATS = {"f32": 0, "bf16": 1, "asym": 2}  # qg_w4_format
+_W4_GROUP_BYTES = (4, 2, 8)
 _DTYPES = {}                                   # torch dtype -> qg_dtype
 
 
-def _launch(fn, stream, tensors, args):
-    """Call fn(*args, stream) on the device that holds `tensors` (None entries
-    are skipped), on that device's current stream unless one is given."""
+def _torch():
     import torch
-    dev = tensors[0].get_device()
-    for t in tensors:
+    if not _DTYPES:
+        _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    return torch
+
+
+def _launch(fn, stream, dev, others, args):
+    """Call fn(*args, stream) on device `dev`, where every tensor of `others`
+    (None entries are skipped) has to be too; the stream is that device's
+    current one unless one is given.  One call from Python costs about as much
+    as the smallest kernels here run, so this and the checks below touch each
+    tensor as little as they can."""
+    torch = _torch()
+    for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{fn.__name__}: the tensors are not on one device")
     if dev < 0:
         raise ValueError(f"{fn.__name__}: expected CUDA tensors")
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream))
-    elif stream is None:
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if stream is not None:
+        stream = _stream(stream)
+    else:  # current_stream(dev) without building a Stream object
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, stream)
     else:
-        rc = fn(*args, _stream(stream))
-    if rc != QG_OK:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc:
         raise QGError(rc, fn.__name__)
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _rows(t, dtype, what):
+    """(rows, length, row stride) of a 2-D row-major tensor of that dtype."""
+    st = t.stride()
+    if len(st) != 2 or t.dtype is not dtype:
+        raise ValueError(f"{what}: expected 2-D rows of {dtype}, got {t.dim()}-D {t.dtype}")
+    n, k = t.shape
+    ld, one = st
+    if one != 1 and k != 1:
+        raise ValueError(f"{what}: expected a row-major view")
+    if n <= 1 and ld < k:  # the stride of a single row says nothing
+        ld = k
+    return n, k, ld
 
 
-def _row_dtype(*rows):
-    import torch
-    if not _DTYPES:
-        _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    code = _DTYPES.get(rows[0].dtype)
-    _need(code is not None, "rows are float32, bfloat16 or float16")
-    for r in rows:
-        _need(r.dtype == rows[0].dtype, "the rows have one dtype")
-        _need(r.dim() == 2 and (r.stride(1) == 1 or r.shape[1] == 1), "expected row-major 2-D rows")
-    return code
+def _check_dense(t, dtype, shape, what):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {dtype} {shape}")
 
 
-def _row_ld(t):
-    """Row stride of a 2-D view; of a single row, at least its length."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _int32(t, shape, what):
-    import torch
-    _need(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape,
-          f"{what}: expected contiguous int32 {shape}")
-
-
-def _float32(t, shape, what):
-    import torch
-    if t is not None:
-        _need(t.dtype == torch.float32 and t.is_contiguous() and tuple(t.shape) == shape,
-              f"{what}: expected contiguous float32 {shape}")
+def _pos_topk(pos, T):
+    torch = _torch()
+    if pos.dim() != 2:
+        raise ValueError("pos: expected [T][topk]")
+    topk = pos.shape[1]
+    _check_dense(pos, torch.int32, (T, topk), "pos")
+    return topk
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _w4_bytes(N, K, fmt):
-    return N * (K // 2) + N * (K // 32) * (4, 2, 8)[fmt]
-
-
-def _product_rows(x, y, packed_w, weights):
-    import torch
+def _w4_format(weights):
     fmt = W4_FORMATS.get(weights)
-    _need(fmt is not None, f"weights: expected one of {sorted(W4_FORMATS)}")
-    _need(x.dtype == torch.bfloat16, "the rows are bfloat16")
-    _row_dtype(x, y)
-    _need(packed_w.dtype == torch.uint8, "packed_w: expected uint8")
+    if fmt is None:
+        raise ValueError(f"weights: expected one of {sorted(W4_FORMATS)}")
     return fmt
 
 
-def _experts_packed(packed_w, E, N, K, fmt):
-    """Bytes from one expert's packed matrix to the next."""
-    _need(packed_w.dim() == 2 and packed_w.shape[0] == E and packed_w.stride(1) == 1
-          and packed_w.shape[1] >= _w4_bytes(N, K, fmt),
-          "packed_w: expected uint8 [E][bytes] that hold a packed matrix each")
-    return max(packed_w.stride(0), packed_w.shape[1])
+def _w4_matrix(packed_w, N, K, fmt):
+    """Checks one packed [N][K] matrix."""
+    if packed_w.dtype is not _torch().uint8 or not packed_w.is_contiguous() or \
+            packed_w.numel() < N * (K // 2) + N * (K // 32) * _W4_GROUP_BYTES[fmt]:
+        raise ValueError("packed_w: expected contiguous uint8 that holds a packed [N][K] matrix")
+
+
+def _w4_experts(packed_w, N, K, fmt):
+    """(E, bytes from one packed matrix to the next) of [E][bytes]."""
+    E, n, ld = _rows(packed_w, _torch().uint8, "packed_w")
+    if n < N * (K // 2) + N * (K // 32) * _W4_GROUP_BYTES[fmt]:
+        raise ValueError("packed_w: expected uint8 [E][bytes] that hold a packed [N][K] matrix each")
+    return E, ld
 
 
 def qgemm_a16w4_bf16(x, packed_w, y, bias=None, weights="f32", stream=None):
     """y = x @ W^T + bias; x bf16 [M][K], y bf16 [M][N], W packed by pack_w4_g32
     (weights="f32"), pack_w4_g32_bf16 ("bf16") or pack_w4_g32_asym ("asym")."""
-    fmt = _product_rows(x, y, packed_w, weights)
-    (M, K), N = x.shape, y.shape[1]
-    _need(y.shape[0] == M, "x and y have the same number of rows")
-    _need(packed_w.is_contiguous() and packed_w.numel() >= _w4_bytes(N, K, fmt),
-          "packed_w is smaller than a packed [N][K] matrix")
-    _float32(bias, (N,), "bias")
-    _launch(lib.qgemm_a16w4_bf16, stream, (x, packed_w, y, bias),
-            (M, N, K, x.data_ptr(), _row_ld(x), packed_w.data_ptr(), fmt, _addr(bias),
-             y.data_ptr(), _row_ld(y)))
+    torch = _torch()
+    fmt = _w4_format(weights)
+    M, K, ldx = _rows(x, torch.bfloat16, "x")
+    My, N, ldy = _rows(y, torch.bfloat16, "y")
+    if My != M:
+        raise ValueError("x and y have the same number of rows")
+    _w4_matrix(packed_w, N, K, fmt)
+    if bias is not None:
+        _check_dense(bias, torch.float32, (N,), "bias")
+    _launch(lib.qgemm_a16w4_bf16, stream, x.get_device(), (packed_w, y, bias),
+            (M, N, K, x.data_ptr(), ldx, packed_w.data_ptr(), fmt, _addr(bias), y.data_ptr(), ldy))
 
 
 def qgemm_a16w4_bf16_experts(x, offsets, packed_w, y, src=None, topk=1, bias=None, weights="f32",
                              stream=None):
     """y[p] = W[e] @ x[src[p] // topk] + bias[e] (x[p] without src) for the rows
     p of expert e, offsets[e] <= p < offsets[e+1]; packed_w uint8 [E][bytes]."""
-    fmt = _product_rows(x, y, packed_w, weights)
-    (S, N), K, E = y.shape, x.shape[1], packed_w.shape[0]
-    step = _experts_packed(packed_w, E, N, K, fmt)
-    _int32(offsets, (E + 1,), "offsets")
+    torch = _torch()
+    fmt = _w4_format(weights)
+    rows, K, ldx = _rows(x, torch.bfloat16, "x")
+    S, N, ldy = _rows(y, torch.bfloat16, "y")
+    E, step = _w4_experts(packed_w, N, K, fmt)
+    _check_dense(offsets, torch.int32, (E + 1,), "offsets")
     if src is not None:
-        _int32(src, (S,), "src")
-    _float32(bias, (E, N), "bias")
-    _launch(lib.qgemm_a16w4_bf16_experts, stream, (x, offsets, packed_w, y, src, bias),
-            (E, S, N, K, x.data_ptr(), _row_ld(x), x.shape[0], _addr(src), topk,
-             offsets.data_ptr(), packed_w.data_ptr(), step, fmt, _addr(bias), y.data_ptr(),
-             _row_ld(y)))
+        _check_dense(src, torch.int32, (S,), "src")
+    if bias is not None:
+        _check_dense(bias, torch.float32, (E, N), "bias")
+    _launch(lib.qgemm_a16w4_bf16_experts, stream, x.get_device(), (offsets, packed_w, y, src, bias),
+            (E, S, N, K, x.data_ptr(), ldx, rows, _addr(src), topk, offsets.data_ptr(),
+             packed_w.data_ptr(), step, fmt, _addr(bias), y.data_ptr(), ldy))
+
+
+def qgemm_a16w4_bf16_grad_x(dy, packed_w, dx, weights="f32", stream=None):
+    """dx = dy @ W, the gradient of qgemm_a16w4_bf16 with respect to x; dy bf16
+    [M][N], dx bf16 [M][K]."""
+    torch = _torch()
+    fmt = _w4_format(weights)
+    M, N, lddy = _rows(dy, torch.bfloat16, "dy")
+    Mx, K, lddx = _rows(dx, torch.bfloat16, "dx")
+    if Mx != M:
+        raise ValueError("dy and dx have the same number of rows")
+    _w4_matrix(packed_w, N, K, fmt)
+    _launch(lib.qgemm_a16w4_bf16_grad_x, stream, dy.get_device(), (packed_w, dx),
+            (M, N, K, dy.data_ptr(), lddy, packed_w.data_ptr(), fmt, dx.data_ptr(), lddx))
+
+
+def qgemm_a16w4_bf16_experts_grad_x(dy, offsets, packed_w, dx, weights="f32", stream=None):
+    """dx[p] = dy[p] @ W[e] for the rows p of expert e (sorted order), the
+    gradient of qgemm_a16w4_bf16_experts with respect to each row's input."""
+    torch = _torch()
+    fmt = _w4_format(weights)
+    S, N, lddy = _rows(dy, torch.bfloat16, "dy")
+    Sx, K, lddx = _rows(dx, torch.bfloat16, "dx")
+    if Sx != S:
+        raise ValueError("dy and dx have the same number of rows")
+    E, step = _w4_experts(packed_w, N, K, fmt)
+    _check_dense(offsets, torch.int32, (E + 1,), "offsets")
+    _launch(lib.qgemm_a16w4_bf16_experts_grad_x, stream, dy.get_device(), (offsets, packed_w, dx),
+            (E, S, N, K, dy.data_ptr(), lddy, offsets.data_ptr(), packed_w.data_ptr(), step, fmt,
+             dx.data_ptr(), lddx))
 
 
 def qg_sort_by_expert_workspace_bytes(T, topk, E):
@@ -548,65 +591,83 @@ def qg_sort_by_expert_workspace_bytes(T, topk, E):
 def qg_sort_by_expert(ids, offsets, src, pos, workspace=None, stream=None):
     """Stable order of the entries ids [T][topk] by expert: offsets [E+1],
     src [T*topk] (entry at a sorted position), pos [T][topk] (-1: no expert)."""
-    import torch
-    T, topk = ids.shape
-    E = offsets.shape[0] - 1
-    _need(ids.dtype == torch.int32 and (ids.stride(1) == 1 or topk == 1), "ids: expected int32 rows")
-    _int32(offsets, (E + 1,), "offsets")
-    _int32(src, (T * topk,), "src")
-    _int32(pos, (T, topk), "pos")
-    need = lib.qg_sort_by_expert_workspace_bytes(T, topk, E)
-    if need and workspace is None:
-        workspace = _empty_bytes(need, ids.device)
-    _launch(lib.qg_sort_by_expert, stream, (ids, offsets, src, pos, workspace),
-            (T, topk, E, ids.data_ptr(), _row_ld(ids), offsets.data_ptr(), src.data_ptr(),
-             pos.data_ptr(), _addr(workspace),
-             0 if workspace is None else workspace.numel() * workspace.element_size()))
+    torch = _torch()
+    T, topk, ld = _rows(ids, torch.int32, "ids")
+    E = offsets.numel() - 1
+    _check_dense(offsets, torch.int32, (E + 1,), "offsets")
+    _check_dense(src, torch.int32, (T * topk,), "src")
+    _check_dense(pos, torch.int32, (T, topk), "pos")
+    have = 0
+    if workspace is None:
+        have = lib.qg_sort_by_expert_workspace_bytes(T, topk, E)
+        if have:
+            workspace = _empty_bytes(have, ids.device)
+    else:
+        have = workspace.numel() * workspace.element_size()
+    _launch(lib.qg_sort_by_expert, stream, ids.get_device(), (offsets, src, pos, workspace),
+            (T, topk, E, ids.data_ptr(), ld, offsets.data_ptr(), src.data_ptr(), pos.data_ptr(),
+             _addr(workspace), have))
+
+
+def _row_type(t):
+    _torch()
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError("the rows are float32, bfloat16 or float16")
+    return dt
 
 
 def qg_spread_rows(x, pos, xs, stream=None):
     """xs[pos[t, j]] = x[t]; negative positions are left out."""
-    dt = _row_dtype(x, xs)
-    T, N = x.shape
-    topk = pos.shape[1]
-    _int32(pos, (T, topk), "pos")
-    _need(xs.shape[1] == N, "x and xs have rows of one length")
-    _launch(lib.qg_spread_rows, stream, (x, pos, xs),
-            (T, topk, xs.shape[0], N, dt, x.data_ptr(), _row_ld(x), pos.data_ptr(),
-             xs.data_ptr(), _row_ld(xs)))
+    dt = _row_type(x)
+    T, N, ldx = _rows(x, x.dtype, "x")
+    S, n, ldxs = _rows(xs, x.dtype, "xs")
+    if n != N:
+        raise ValueError("x and xs have rows of one length")
+    _launch(lib.qg_spread_rows, stream, x.get_device(), (pos, xs),
+            (T, _pos_topk(pos, T), S, N, dt, x.data_ptr(), ldx, pos.data_ptr(), xs.data_ptr(), ldxs))
 
 
 def qg_combine_rows(ys, pos, y, weights=None, stream=None):
     """y[t] = sum_j weights[t, j] * ys[pos[t, j]] (weights None: 1)."""
-    dt = _row_dtype(ys, y)
-    T, N = y.shape
-    topk = pos.shape[1]
-    _int32(pos, (T, topk), "pos")
-    _float32(weights, (T, topk), "weights")
-    _need(ys.shape[1] == N, "ys and y have rows of one length")
-    _launch(lib.qg_combine_rows, stream, (ys, pos, y, weights),
-            (T, topk, ys.shape[0], N, dt, ys.data_ptr(), _row_ld(ys), pos.data_ptr(),
-             _addr(weights), y.data_ptr(), _row_ld(y)))
+    dt = _row_type(y)
+    T, N, ldy = _rows(y, y.dtype, "y")
+    S, n, ldys = _rows(ys, y.dtype, "ys")
+    if n != N:
+        raise ValueError("ys and y have rows of one length")
+    topk = _pos_topk(pos, T)
+    if weights is not None:
+        _check_dense(weights, _torch().float32, (T, topk), "weights")
+    _launch(lib.qg_combine_rows, stream, y.get_device(), (pos, ys, weights),
+            (T, topk, S, N, dt, ys.data_ptr(), ldys, pos.data_ptr(), _addr(weights), y.data_ptr(),
+             ldy))
 
 
 def qg_combine_rows_grad(dy, ys, pos, weights, dys, dw, stream=None):
     """Gradients of qg_combine_rows: dys[pos[t, j]] = weights[t, j] * dy[t] and
     dw[t, j] = <dy[t], ys[pos[t, j]]>.  dys or dw (then also ys) may be None."""
-    rows = [r for r in (dy, ys, dys) if r is not None]
-    dt = _row_dtype(*rows)
-    T, N = dy.shape
-    topk = pos.shape[1]
-    _int32(pos, (T, topk), "pos")
-    _float32(weights, (T, topk), "weights")
-    _float32(dw, (T, topk), "dw")
-    _need(dw is None or ys is not None, "dw needs ys")
-    _need(all(r.shape[1] == N for r in rows), "dy, ys and dys have rows of one length")
-    S = (ys if ys is not None else dys if dys is not None else dy).shape[0]
-    _need(ys is None or dys is None or ys.shape[0] == dys.shape[0], "ys and dys have the same rows")
-    _launch(lib.qg_combine_rows_grad, stream, (dy, ys, pos, weights, dys, dw),
-            (T, topk, S, N, dt, dy.data_ptr(), _row_ld(dy), _addr(ys),
-             N if ys is None else _row_ld(ys), pos.data_ptr(), _addr(weights), _addr(dys),
-             N if dys is None else _row_ld(dys), _addr(dw)))
+    dt = _row_type(dy)
+    T, N, lddy = _rows(dy, dy.dtype, "dy")
+    topk = _pos_topk(pos, T)
+    if weights is not None:
+        _check_dense(weights, _torch().float32, (T, topk), "weights")
+    if dw is not None:
+        _check_dense(dw, _torch().float32, (T, topk), "dw")
+        if ys is None:
+            raise ValueError("dw needs ys")
+    S, ldys, lddys = None, N, N
+    if ys is not None:
+        S, n, ldys = _rows(ys, dy.dtype, "ys")
+        if n != N:
+            raise ValueError("dy and ys have rows of one length")
+    if dys is not None:
+        Sd, n, lddys = _rows(dys, dy.dtype, "dys")
+        if n != N or (S is not None and S != Sd):
+            raise ValueError("dys has the rows of ys and the length of dy")
+        S = Sd
+    _launch(lib.qg_combine_rows_grad, stream, dy.get_device(), (pos, ys, weights, dys, dw),
+            (T, topk, S or 0, N, dt, dy.data_ptr(), lddy, _addr(ys), ldys, pos.data_ptr(),
+             _addr(weights), _addr(dys), lddys, _addr(dw)))
 
 
 def exported_symbols():

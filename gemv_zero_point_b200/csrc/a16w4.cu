@@ -20,11 +20,12 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "qg_internal.cuh"
+#include "a16w4.cuh"
 
 namespace qg {
 
 int device_setup_status();
+int a16w4_tc_setup();
 
 namespace {
 
@@ -34,7 +35,6 @@ constexpr int SR = 32;            // weight rows per step (two MMA row tiles)
 constexpr int RP = 2;             // steps per chunk at most: 64 rows per warp
 constexpr int WROWS = SR * RP;
 constexpr int NIB_PITCH = 80;     // 64 bytes of nibbles; the pitch spreads 8 rows over all banks
-constexpr int kRowsMaxE = 1024;
 
 // Bytes of one step in a warp's ring: nibbles, then scales (and zeros) of SR
 // rows x 4 groups.
@@ -87,12 +87,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
 }
 
 // The 8 codes of nibble word w as four bf16 pairs, exact: 0x4300 | u is
@@ -472,7 +466,7 @@ int run_rows_nt(int nt, const RowsArgs& a, cudaStream_t st) {
 
 template <int FMT, int NT>
 int set_rows_smem() {
-  const size_t most = rows_smem(FMT, NT, Ring<FMT, NT>::D, W, kRowsMaxE);
+  const size_t most = rows_smem(FMT, NT, Ring<FMT, NT>::D, W, kA16W4MaxExperts);
   return cudaFuncSetAttribute((const void*)a16w4_rows_kernel<FMT, NT, Ring<FMT, NT>::D>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)most) == cudaSuccess
@@ -494,6 +488,7 @@ int a16w4_setup() {
   int rc = set_rows_smem_nt<QG_W4_F32>();
   if (rc == QG_OK) rc = set_rows_smem_nt<QG_W4_BF16>();
   if (rc == QG_OK) rc = set_rows_smem_nt<QG_W4_ASYM>();
+  if (rc == QG_OK) rc = a16w4_tc_setup();
   return rc;
 }
 
@@ -526,6 +521,13 @@ int64_t packed_bytes(int N, int K, int format) {
   return (int64_t)N * (K / 2) + (int64_t)N * (K / 32) * group;
 }
 
+// Few rows per expert stream the weights past warp MMAs, more go to the
+// tensor cores.
+int launch_product(const A16W4Call& c, cudaStream_t st) {
+  if (cdiv(c.S, c.E) <= 32) return launch_a16w4_rows(c, st);
+  return launch_a16w4_tc(c, false, st);
+}
+
 // Checks of every product: QG_OK when the call can run (S may be 0).
 int product_args(int E, int S, int N, int K, const void* in, int64_t ld_in, int in_cols,
                  const void* packed, int64_t expert_bytes, int format, const float* bias,
@@ -534,7 +536,7 @@ int product_args(int E, int S, int N, int K, const void* in, int64_t ld_in, int 
     return QG_ERR_INVALID_ARG;
   if (format != QG_W4_F32 && format != QG_W4_BF16 && format != QG_W4_ASYM)
     return QG_ERR_INVALID_ARG;
-  if (K % 64 || E > kRowsMaxE) return QG_ERR_UNSUPPORTED;
+  if (K % 64 || E > kA16W4MaxExperts) return QG_ERR_UNSUPPORTED;
   if (S == 0) return QG_OK;
   if (!in || !packed || !out) return QG_ERR_INVALID_ARG;
   if (((uintptr_t)packed & 15) || ((uintptr_t)in & 15) || ld_in % 8 || ((uintptr_t)out & 1) ||
@@ -561,7 +563,41 @@ extern "C" int qgemm_a16w4_bf16(int M, int N, int K, const void* x, int64_t ldx,
   c.in = (const uint16_t*)x; c.ld_in = ldx; c.in_rows = M; c.topk = 1;
   c.packed = (const uint8_t*)packed_w; c.format = format; c.bias = bias;
   c.out = (uint16_t*)y; c.ld_out = ldy;
-  return launch_a16w4_rows(c, (cudaStream_t)stream);
+  return launch_product(c, (cudaStream_t)stream);
+}
+
+extern "C" int qgemm_a16w4_bf16_grad_x(int M, int N, int K, const void* dy, int64_t lddy,
+                                       const void* packed_w, int format, void* dx, int64_t lddx,
+                                       void* stream) {
+  int rc = product_args(1, M, N, K, dy, lddy, N, packed_w, 0, format, nullptr, dx, lddx, K);
+  if (rc != QG_OK || M == 0) return rc;
+  rc = device_setup_status();
+  if (rc != QG_OK) return rc;
+  A16W4Call c{};
+  c.E = 1; c.S = M; c.N = N; c.K = K;
+  c.in = (const uint16_t*)dy; c.ld_in = lddy; c.in_rows = M; c.topk = 1;
+  c.packed = (const uint8_t*)packed_w; c.format = format;
+  c.out = (uint16_t*)dx; c.ld_out = lddx;
+  return launch_a16w4_tc(c, true, (cudaStream_t)stream);
+}
+
+extern "C" int qgemm_a16w4_bf16_experts_grad_x(int E, int S, int N, int K, const void* dy,
+                                               int64_t lddy, const int32_t* offsets,
+                                               const void* packed_w, int64_t expert_bytes,
+                                               int format, void* dx, int64_t lddx,
+                                               void* stream) {
+  int rc = product_args(E, S, N, K, dy, lddy, N, packed_w, expert_bytes, format, nullptr, dx, lddx, K);
+  if (rc != QG_OK || S == 0) return rc;
+  if (!offsets) return QG_ERR_INVALID_ARG;
+  if ((uintptr_t)offsets & 3) return QG_ERR_MISALIGNED;
+  rc = device_setup_status();
+  if (rc != QG_OK) return rc;
+  A16W4Call c{};
+  c.E = E; c.S = S; c.N = N; c.K = K;
+  c.in = (const uint16_t*)dy; c.ld_in = lddy; c.in_rows = S; c.topk = 1;
+  c.offsets = offsets; c.packed = (const uint8_t*)packed_w; c.expert_bytes = expert_bytes;
+  c.format = format; c.out = (uint16_t*)dx; c.ld_out = lddx;
+  return launch_a16w4_tc(c, true, (cudaStream_t)stream);
 }
 
 extern "C" int qgemm_a16w4_bf16_experts(int E, int S, int N, int K, const void* x, int64_t ldx,
@@ -582,5 +618,5 @@ extern "C" int qgemm_a16w4_bf16_experts(int E, int S, int N, int K, const void* 
   c.in = (const uint16_t*)x; c.ld_in = ldx; c.in_rows = x_rows; c.src = src; c.topk = topk;
   c.offsets = offsets; c.packed = (const uint8_t*)packed_w; c.expert_bytes = expert_bytes;
   c.format = format; c.bias = bias; c.out = (uint16_t*)y; c.ld_out = ldy;
-  return launch_a16w4_rows(c, (cudaStream_t)stream);
+  return launch_product(c, (cudaStream_t)stream);
 }

@@ -232,40 +232,6 @@ size_t a8w4_tc_workspace_bytes(int64_t M, int N, int K);
 int launch_a8w4_tc_call(const A8W4TcCall& c, void* ws, size_t ws_bytes, cudaStream_t st);
 
 // ---------------------------------------------------------------------------
-// One call of the weight-only products (bf16 rows x int4 weights), dense
-// (offsets NULL: E = 1, every row is expert 0's) or per expert.  Forward:
-// in [rows][K], out [S][N]; gradient with respect to x: in [S][N], out [S][K].
-// ---------------------------------------------------------------------------
-struct A16W4Call {
-  int E, S, N, K;
-  const uint16_t* in;      // bf16
-  int64_t ld_in;
-  int in_rows;             // rows of `in` (src reaches no further)
-  const int32_t* src;      // sorted row p reads input row src[p] / topk; NULL: row p
-  int topk;
-  const int32_t* offsets;  // [E + 1] or NULL
-  const uint8_t* packed;
-  int64_t expert_bytes;    // from one expert's packed matrix to the next
-  int format;              // QG_W4_*
-  const float* bias;       // [E][N] or NULL
-  uint16_t* out;           // bf16
-  int64_t ld_out;
-};
-int launch_a16w4_rows(const A16W4Call& c, cudaStream_t st);  // few rows (a16w4.cu)
-
-// Rows [start, start + count) of expert e; a range that is not inside [0, S)
-// is an error of the caller's: recorded, then no rows.
-__device__ __forceinline__ int2 expert_range(const int32_t* offsets, int e, int S, int* status) {
-  if (!offsets) return make_int2(0, S);
-  const int a = offsets[e], b = offsets[e + 1];
-  if (a < 0 || b < a || b > S) {
-    record_error(status, QG_ERR_INVALID_ARG);
-    return make_int2(0, 0);
-  }
-  return make_int2(a, b - a);
-}
-
-// ---------------------------------------------------------------------------
 // Integer dot products
 // ---------------------------------------------------------------------------
 // sum_b a.u8[b] * b.s8[b] + c  (a unsigned bytes, b signed bytes)

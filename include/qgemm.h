@@ -423,8 +423,10 @@ int qconv2d_f32_dyn_a8w4(int Nb, int H, int W, int Cin, int Cout, int KH, int KW
  *   packed_w: 16-byte aligned, in the packing that `format` names (qg_w4_format)
  *   bias: f32 [N] or NULL;  y: bf16 [M][ldy] (ldy >= N), any alignment
  * K % 64 == 0 (else QG_ERR_UNSUPPORTED); M >= 0, any N >= 1.  No workspace.
- * Sums are held in f32 and y is rounded once.  Rows of x do not mix: a
- * non-finite value in one row reaches that row of y alone.
+ * Sums are held in f32 and y is rounded once.  A few rows use the exact int4
+ * codes; for many rows each weight w[n,k] is rounded to bf16 first (half a
+ * step, 2^-8 of it).  Rows of x do not mix: a non-finite value in one row
+ * reaches that row of y alone.
  * ------------------------------------------------------------------------ */
 typedef enum {
   QG_W4_F32 = 0,  /* pack_w4_g32: f32 group scales */
@@ -454,6 +456,24 @@ int qgemm_a16w4_bf16_experts(int E, int S, int N, int K, const void* x, int64_t 
                              const int32_t* src, int topk, const int32_t* offsets,
                              const void* packed_w, int64_t expert_bytes, int format,
                              const float* bias, void* y, int64_t ldy, void* stream);
+
+/*
+ * Gradients of the two products with respect to their rows, for training
+ * around frozen int4 weights (which have no gradient):
+ *   dx[m,k] = sum_n dy[m,n] * w[n,k]
+ *   dy: bf16 [M][lddy] (lddy >= N), 16-byte aligned, lddy % 8 == 0
+ *   dx: bf16 [M][lddx] (lddx >= K), any alignment
+ * and per expert for the rows in sorted order, dx[p] = W[e]^T @ dy[p]; the sum
+ * over a token's entries is then qg_combine_rows(dx, pos, weights NULL).
+ * Other arguments, limits and errors as for the products.
+ */
+int qgemm_a16w4_bf16_grad_x(int M, int N, int K, const void* dy, int64_t lddy,
+                            const void* packed_w, int format, void* dx, int64_t lddx,
+                            void* stream);
+int qgemm_a16w4_bf16_experts_grad_x(int E, int S, int N, int K, const void* dy, int64_t lddy,
+                                    const int32_t* offsets, const void* packed_w,
+                                    int64_t expert_bytes, int format, void* dx, int64_t lddx,
+                                    void* stream);
 
 /* ------------------------------------------------------------------------
  * Tokens in the order of their experts, and back.  The pages have no

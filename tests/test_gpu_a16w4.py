@@ -132,6 +132,67 @@ def test_experts_match_oracle(lib, T, topk, E, N, K, drop, hot, fmt, gathered):
     assert (y[offsets[E]:] == 7.0).all()      # rows behind the last expert stay
 
 
+GRADS = [(1, 8, 64), (3, 64, 128), (17, 72, 192), (64, 128, 64), (100, 1000, 832), (129, 136, 448),
+         (256, 512, 1024), (300, 520, 576), (513, 2056, 320), (33, 4096, 256)]
+
+
+@pytest.mark.parametrize("M,N,K", GRADS)
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "asym"])
+def test_linear_grad_matches_oracle(lib, M, N, K, fmt):
+    rng = np.random.default_rng(M + N + K)
+    qw, sw, zw = C.weights(rng, N, K, fmt)
+    dy = C.bf16_round(rng.standard_normal((M, N)))
+    dx = torch.full((M, K + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+    lib.qgemm_a16w4_bf16_grad_x(_bf16(dy), C.pack(lib, torch, qw, sw, zw, fmt), dx[:, :K], weights=fmt)
+    wt = C.real(qw, sw, zw).T
+    ref = oracle.a16w4(dy, wt)
+    C.assert_close(_np(dx)[:, :K], ref, C.tolerance(dy.astype(np.float64), wt, ref), f"{M}x{N}x{K} {fmt}")
+    assert (_np(dx)[:, K:] == 7.0).all()
+
+
+def test_linear_grad_against_differences(lib):
+    """The gradient of sum(y * dy) by central differences of the oracle's y;
+    linear in x, so the difference is exact up to its 64-bit rounding and the
+    rounding of dx (tolerance of the product)."""
+    rng = np.random.default_rng(2)
+    M, N, K = 40, 72, 128
+    qw, sw, zw = C.weights(rng, N, K, "asym")
+    w = C.real(qw, sw, zw)
+    dy = C.bf16_round(rng.standard_normal((M, N)))
+    x = rng.standard_normal((M, K))
+    dx = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    lib.qgemm_a16w4_bf16_grad_x(_bf16(dy), C.pack(lib, torch, qw, sw, zw, "asym"), dx, weights="asym")
+    tol = C.tolerance(dy.astype(np.float64), w.T, dy.astype(np.float64) @ w)
+    for m, k in [(0, 0), (39, 127), (7, 64), (20, 31)]:
+        up, dn = x.copy(), x.copy()
+        up[m, k] += 0.5
+        dn[m, k] -= 0.5
+        diff = ((oracle.a16w4(up, w) - oracle.a16w4(dn, w)) * dy).sum()
+        assert abs(diff - float(dx[m, k])) <= tol[m, k] + 1e-10
+
+
+@pytest.mark.parametrize("T,topk,E,N,K,drop,hot", EXPERTS)
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "asym"])
+def test_experts_grad_matches_oracle(lib, T, topk, E, N, K, drop, hot, fmt):
+    rng, (qw, sw, zw), packed, offsets, src, off_d, _ = _experts(
+        lib, T, topk, E, N, K, fmt, drop, hot, T + K)
+    S = T * topk
+    ld = -(-N // 8) * 8
+    dy = C.bf16_round(rng.standard_normal((S, N)))
+    dyd = torch.full((S, ld), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dyd[:, :N] = _bf16(dy)
+    dx = torch.full((S, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    lib.qgemm_a16w4_bf16_experts_grad_x(dyd[:, :N], off_d, packed, dx, weights=fmt)
+    dx = _np(dx)
+    for e in range(E):
+        a, b = offsets[e], offsets[e + 1]
+        if a < b:
+            wt = C.real(qw[e], sw[e], None if zw is None else zw[e]).T
+            ref = oracle.a16w4(dy[a:b], wt)
+            C.assert_close(dx[a:b], ref, C.tolerance(dy[a:b].astype(np.float64), wt, ref), f"expert {e}")
+    assert (dx[offsets[E]:] == 7.0).all()
+
+
 def test_experts_without_any_row(lib):
     """No entry has an expert: nothing is written."""
     rng = np.random.default_rng(5)
