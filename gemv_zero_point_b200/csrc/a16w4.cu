@@ -9,13 +9,16 @@
 // With few rows the weights' bytes bound the call, so the kernel is a stream
 // over the packed weights that must not run out of issue slots: at the
 // measured copy bandwidth an SM receives about 37 weights per cycle, which
-// leaves 3.4 lane instructions per weight.  A scalar form (unpack, convert,
-// multiply) takes most of them for one row and grows with the rows.  Warp
-// MMAs (m16n8k16) take 16 weight rows x 8 token rows at once: the cost per
-// weight is the unpacking (about 1.4 instructions), whatever the number of
-// tokens up to 8.  The MMAs see the exact codes, each group's two MMAs start
-// from zero, and the group scale is applied to their f32 result, so nothing
-// is rounded below f32 before y.
+// leaves 3.4 issue slots per weight, and logic, shifts and packed bf16
+// arithmetic take two each.  Warp MMAs (m16n8k16, 8 cycles a sub-partition)
+// take 16 weight rows x 8 token rows at once, so the cost per weight is the
+// unpacking, whatever the number of tokens up to 8.
+//   - A code c goes in as 128 + u, u = c + 8: two nibbles become a pair of
+//     bf16 values with one logic and one byte permute instruction.
+//   - 128 + u = c + 136, so a group's sums start at -136 X, X = sum x, formed
+//     by MMAs with the constant once per chunk for all weight rows.
+//   - The group scale is applied to the f32 sums of the group: nothing is
+//     rounded below f32 before y (the 136 costs the sums 5 of their 24 bits).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -31,19 +34,21 @@ namespace {
 
 constexpr int W = 8;              // warps per CTA
 constexpr int KC = 128;           // K per chunk: 4 groups, 64 nibble bytes a row
-constexpr int SR = 32;            // weight rows per step (two MMA row tiles)
-constexpr int RP = 2;             // steps per chunk at most: 64 rows per warp
-constexpr int WROWS = SR * RP;
-constexpr int NIB_PITCH = 80;     // 64 bytes of nibbles; the pitch spreads 8 rows over all banks
+constexpr int RT = 4;             // 16-row tiles of a run and row warp
+constexpr int WROWS = 16 * RT;
+constexpr int D = 2;              // chunks in a warp's ring
+constexpr int kMinRows = 8;       // fewest weight rows that a CTA takes
+constexpr int kXParts = 16;       // CTAs that prefetch a dense call's rows
 
-// Bytes of one step in a warp's ring: nibbles, then scales (and zeros) of SR
-// rows x 4 groups.
+// Bytes of one chunk in a warp's ring: nibbles (their 16-byte parts turned by
+// row / 2, so eight rows of a part lie in eight bank groups), then scales
+// (and zeros) of WROWS rows x 4 groups.
 template <int FMT>
-struct Step {
+struct Slot {
   static constexpr int SCL = FMT == QG_W4_BF16 ? 8 : 16;  // scale bytes per row
-  static constexpr int OFF_SCL = SR * NIB_PITCH;
-  static constexpr int OFF_ZERO = OFF_SCL + SR * SCL;
-  static constexpr int BYTES = OFF_ZERO + (FMT == QG_W4_ASYM ? SR * 16 : 0);
+  static constexpr int OFF_SCL = WROWS * 64;
+  static constexpr int OFF_ZERO = OFF_SCL + WROWS * SCL;
+  static constexpr int BYTES = OFF_ZERO + (FMT == QG_W4_ASYM ? WROWS * 16 : 0);
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -60,12 +65,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -79,23 +78,56 @@ __device__ __forceinline__ float4 lds128f(uint32_t a) {
                : "memory");
   return v;
 }
+// Four 8 x 16-byte blocks: register m of lane (g, t) is word t of row g of block m.
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+// d = a * b + {c0, c1, c0, c1} (m16n8k16)
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The 8 codes of nibble word w as four bf16 pairs, exact: 0x4300 | u is
-// 128 + u, less 136 is u - 8.  Pair order: codes (0,2), (4,6), (1,3), (5,7).
+// The 8 codes of nibble word w in their order as bf16 pairs 128 + u, u = code + 8.
 __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&p)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t m = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(m), "r"(0x43084308u));
+  const uint32_t L = w & 0x0F0F0F0Fu, H = (w >> 4) & 0x0F0F0F0Fu;
+  p[0] = prmt(L, 0x43434343u, 0x5140u);
+  p[1] = prmt(L, 0x43434343u, 0x5342u);
+  p[2] = prmt(H, 0x43434343u, 0x5140u);
+  p[3] = prmt(H, 0x43434343u, 0x5342u);
+}
+
+// L2 prefetch of the 16-byte-aligned interior of [p, p + bytes).
+__device__ __forceinline__ void prefetch_l2(const void* p, int64_t bytes) {
+  const uintptr_t b = ((uintptr_t)p + 15) & ~(uintptr_t)15;
+  const uintptr_t e = ((uintptr_t)p + (uintptr_t)bytes) & ~(uintptr_t)15;
+  if (e > b) bulk_prefetch_l2((const void*)b, (uint32_t)(e - b));
+}
+
+// q = v / d and the rest r, by 32-bit division where v allows it.
+__device__ __forceinline__ void divide(int64_t v, int d, int64_t& q, int64_t& r) {
+  if (v <= 0x7FFFFFFF) {
+    q = (uint32_t)v / (uint32_t)d;
+    r = (uint32_t)v - (uint32_t)q * (uint32_t)d;
+  } else {
+    q = v / d;
+    r = v - q * d;
   }
 }
 
@@ -106,298 +138,421 @@ struct RowsArgs {
   A16W4Call c;
   int chunks;        // ceil(K / KC)
   int wk;            // warps that split K; W / wk warps split the rows
-  int min_rows;      // fewest rows a CTA takes
+  int share, more;   // dense: 8-row blocks of a CTA, and how many CTAs take one more
 };
 
 // A run: consecutive weight rows of one pass, at most WROWS per row warp.
 struct Run {
-  int e, r0, rows, p0, np;  // expert, first weight row, rows, first sorted row, token rows
+  int e, pass, r0, rows;  // expert, its pass, first weight row, rows
+  int64_t left;           // virtual rows of this CTA from r0 on
+  int base, nrows;        // this warp's rows of the run
 };
 
-// Position of a warp in its steps: run, chunk, step within the chunk.
-struct Cursor {
-  int64_t v;   // virtual row where the run starts
-  Run run;
-  int base, nrows, steps;  // this warp's rows of the run and its steps per chunk
-  int chunk, step;
-  bool done;
+// The runs of one CTA.  DENSE: one matrix and at most one pass, so they
+// follow from the CTA's number alone and the first loads leave at once.
+// Otherwise the passes (of `per` tokens) of every expert are counted first,
+// from the offsets that the work before this call has written.
+template <bool DENSE>
+struct Shares {
+  const RowsArgs& a;
+  const int* pre;    // [E + 1] passes before expert e
+  const int* start;  // [E] first sorted row
+  const int* count;  // [E] rows
+  const int per, wr, rw;
+  int64_t v0, v1;    // this CTA's virtual rows
+
+  __device__ __forceinline__ Shares(const RowsArgs& a_, int per_, int* pre_, int* start_, int* count_,
+                                    int* status)
+      : a(a_), pre(pre_), start(start_), count(count_), per(per_), wr(W / a_.wk),
+        rw((int)(threadIdx.x >> 5) / a_.wk) {
+    const A16W4Call& c = a.c;
+    if (DENSE) {
+      v0 = 8 * ((int64_t)a.share * blockIdx.x + min(a.more, (int)blockIdx.x));
+      v1 = min64(v0 + 8 * (a.share + ((int)blockIdx.x < a.more ? 1 : 0)), c.N);
+      return;
+    }
+    const int lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int e = threadIdx.x; e < c.E; e += W * 32) {
+      const int2 r = expert_range(c.offsets, e, c.S, status);
+      start_[e] = r.x;
+      count_[e] = r.y;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      int carry = 0;
+      for (int b = 0; b < c.E; b += 32) {
+        const int e = b + lane;
+        const int own = e < c.E ? (count_[e] + per - 1) / per : 0;
+        int x = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (e < c.E) pre_[e] = carry + x - own;
+        carry += __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (lane == 0) pre_[c.E] = carry;
+    }
+    __syncthreads();
+    const int64_t total = (int64_t)pre[c.E] * c.N;
+    if (total < (int64_t)gridDim.x * kMinRows) {
+      v0 = min64(total, (int64_t)blockIdx.x * kMinRows);
+      v1 = min64(total, v0 + kMinRows);
+    } else {
+      // shares differ by one row at most
+      int64_t q, r;
+      divide(total, (int)gridDim.x, q, r);
+      v0 = q * blockIdx.x + min64(r, blockIdx.x);
+      v1 = v0 + q + (blockIdx.x < r ? 1 : 0);
+    }
+  }
+
+  // the rest of a run, its start known
+  __device__ __forceinline__ void shape(Run& r) const {
+    r.rows = (int)min64(min64(a.c.N - r.r0, r.left), (int64_t)WROWS * wr);
+    const int share = wr == 1 ? r.rows : ((r.rows + wr - 1) / wr + 15) & ~15;
+    r.base = rw * share;
+    r.nrows = max(0, min(r.rows - r.base, share));
+  }
+  __device__ __forceinline__ Run first() const {
+    Run r;
+    r.e = r.pass = r.r0 = r.rows = r.base = r.nrows = 0;
+    r.left = v1 - v0;
+    if (r.left <= 0) return r;
+    if (DENSE) {
+      r.r0 = (int)v0;
+    } else {
+      int64_t u64, r064;
+      divide(v0, a.c.N, u64, r064);
+      const int u = (int)u64;
+      int lo = 0, hi = a.c.E - 1;  // last expert with pre[e] <= u: the one that has pass u
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= u) lo = mid; else hi = mid - 1;
+      }
+      r.e = lo;
+      r.pass = u - pre[lo];
+      r.r0 = (int)r064;
+    }
+    shape(r);
+    return r;
+  }
+  __device__ __forceinline__ void next(Run& r) const {
+    r.left -= r.rows;
+    if (r.left <= 0) {
+      r.nrows = 0;
+      return;
+    }
+    r.r0 += r.rows;
+    if (!DENSE && r.r0 == a.c.N) {
+      r.r0 = 0;
+      if (++r.pass == pre[r.e + 1] - pre[r.e]) {
+        r.pass = 0;
+        do ++r.e; while (pre[r.e + 1] == pre[r.e]);  // left > 0: one follows
+      }
+    }
+    shape(r);
+  }
+  __device__ __forceinline__ int tokens_from(const Run& r) const {
+    return DENSE ? 0 : start[r.e] + r.pass * per;
+  }
+  __device__ __forceinline__ int tokens(const Run& r) const {
+    return DENSE ? a.c.S : min(count[r.e] - r.pass * per, per);
+  }
+  // row of x that sorted row p reads, -1 (read as zeros) for one outside x
+  __device__ __forceinline__ int input_row(int p, int* status) const {
+    if (DENSE) return p;
+    int row = p;
+    if (a.c.src) {
+      const int s = a.c.src[p];
+      row = s < 0 ? -1 : s / a.c.topk;
+    }
+    if (row < 0 || row >= a.c.in_rows) {
+      record_error(status, QG_ERR_INVALID_ARG);
+      return -1;
+    }
+    return row;
+  }
+  // one whole run into L2, and on to the next
+  __device__ __forceinline__ void prefetch(Run& r, int sb, int64_t zoff, bool zeros) const {
+    if (r.left <= 0) return;
+    const int rowb = a.c.K >> 1, G = a.c.K >> 5;
+    const uint8_t* wq = a.c.packed + (int64_t)r.e * a.c.expert_bytes;
+    prefetch_l2(wq + (int64_t)r.r0 * rowb, (int64_t)r.rows * rowb);
+    const uint8_t* s = wq + (int64_t)a.c.N * rowb + (int64_t)r.r0 * G * sb;
+    prefetch_l2(s, (int64_t)r.rows * G * sb);
+    if (zeros) prefetch_l2(s + zoff, (int64_t)r.rows * G * sb);
+    next(r);
+  }
 };
 
-template <int FMT, int NT, int D>
+// Dense: x into L2 while the work before this call ends (a prefetch cannot
+// return stale data), one part of one row from each of the first CTAs.
+__device__ __forceinline__ void prefetch_x(const A16W4Call& c) {
+  if ((int)threadIdx.x < c.S && blockIdx.x < kXParts) {
+    const int64_t k0 = (int64_t)c.K * blockIdx.x / kXParts, k1 = (int64_t)c.K * (blockIdx.x + 1) / kXParts;
+    prefetch_l2(c.in + (int64_t)threadIdx.x * c.ld_in + k0, (k1 - k0) * 2);
+  }
+}
+
+// y of one run from the partial sums [K warp][token of `per`][row].
+__device__ __forceinline__ void sum_and_store(const A16W4Call& c, const Run& at, int p0, int np,
+                                              int per, int wk, const float* part, int prows) {
+  for (int o = threadIdx.x; o < at.rows * np; o += W * 32) {
+    const int tok = np == 1 ? 0 : o / at.rows, r = o - tok * at.rows;
+    const float* d = part + (size_t)tok * prows + r;
+    float s = 0.0f;
+    for (int k = 0; k < wk; ++k) s += d[(size_t)k * per * prows];
+    const int n = at.r0 + r;
+    if (c.bias) s += __ldg(c.bias + (int64_t)at.e * c.N + n);
+    c.out[(int64_t)(p0 + tok) * c.ld_out + n] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The kernel.  Nibbles and scales come through a ring in shared
+// memory that each warp keeps for itself (cp.async, no barriers), and
+// ldmatrix hands every lane the nibble words of its fragment rows.  The warps
+// of a CTA split K; their sums meet in shared memory at the end of a run.
+// ---------------------------------------------------------------------------
+// NT: MMA column blocks (8 tokens) per pass.
+template <int FMT, int NT, bool DENSE>
 __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1)
-    a16w4_rows_kernel(const RowsArgs a, int* status) {
-  using St = Step<FMT>;
+    a16w4_rows_kernel(const __grid_constant__ RowsArgs a, int* status) {
+  using Sl = Slot<FMT>;
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ int64_t s_total;
   const A16W4Call& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;  // MMA fragment coordinates
-  const int K = c.K, N = c.N, G = K >> 5;
+  const int K = c.K, N = c.N, G = K >> 5, rowb = K >> 1;
   const int wk = a.wk, wr = W / wk;
   const int kw = warp % wk, rw = warp / wk;
+  constexpr int SB = FMT == QG_W4_BF16 ? 2 : 4;
   // shared memory: rings, partial sums, expert tables
   const int prows = WROWS * wr + 4;  // pitch of a token's partial sums; +4 spreads the banks
-  const uint32_t ring = smem_u32(sm) + (uint32_t)(warp * D * St::BYTES);
-  float* part = reinterpret_cast<float*>(sm + W * D * St::BYTES);
+  const uint32_t ring = smem_u32(sm) + (uint32_t)(warp * D * Sl::BYTES);
+  float* part = reinterpret_cast<float*>(sm + W * D * Sl::BYTES);
   int* pre = reinterpret_cast<int*>(part + (size_t)wk * 8 * NT * prows);  // [E + 1] passes before e
   int* start = pre + c.E + 1;
   int* count = start + c.E;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (c.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int e = threadIdx.x; e < c.E; e += W * 32) {
-    const int2 r = expert_range(c.offsets, e, c.S, status);
-    start[e] = r.x;
-    count[e] = r.y;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int carry = 0;
-    for (int b = 0; b < c.E; b += 32) {
-      const int e = b + lane;
-      const int own = e < c.E ? (count[e] + 8 * NT - 1) / (8 * NT) : 0;
-      int x = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (e < c.E) pre[e] = carry + x - own;
-      carry += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) {
-      pre[c.E] = carry;
-      s_total = (int64_t)carry * N;
-    }
-  }
-  __syncthreads();
-  const int64_t total = s_total;
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  int64_t v0, v1;
-  if (per < a.min_rows) {
-    v0 = min64(total, (int64_t)blockIdx.x * a.min_rows);
-    v1 = min64(total, v0 + a.min_rows);
-  } else {
-    // shares differ by one row at most
-    const int64_t q = total / gridDim.x, r = total - q * gridDim.x;
-    v0 = q * blockIdx.x + min64(r, blockIdx.x);
-    v1 = v0 + q + (blockIdx.x < r ? 1 : 0);
-  }
-
+  Shares<DENSE> sh(a, 8 * NT, pre, start, count, status);
+  Run at = sh.first();
   const int ch0 = (int)((int64_t)kw * a.chunks / wk), ch1 = (int)((int64_t)(kw + 1) * a.chunks / wk);
 
-  auto open_run = [&](Cursor& cu) {
-    if (cu.v >= v1) {
-      cu.done = true;
-      return;
-    }
-    const int u = (int)(cu.v / N);
-    int lo = 0, hi = c.E - 1;  // last expert with pre[e] <= u that has passes
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= u) lo = mid; else hi = mid - 1;
-    }
-    cu.run.e = lo;
-    const int pass = u - pre[lo];
-    cu.run.r0 = (int)(cu.v - (int64_t)u * N);
-    cu.run.rows = (int)min64(min64(N - cu.run.r0, v1 - cu.v), (int64_t)WROWS * wr);
-    cu.run.p0 = start[lo] + pass * 8 * NT;
-    cu.run.np = min(count[lo] - pass * 8 * NT, 8 * NT);
-    const int share = ((cu.run.rows + wr - 1) / wr + 15) & ~15;  // rows per row warp
-    cu.base = rw * share;
-    cu.nrows = max(0, min(cu.run.rows - cu.base, share));
-    cu.steps = (cu.nrows + SR - 1) / SR;
-    cu.chunk = ch0;
-    cu.step = 0;
+  // ---- copies into the ring, D - 1 chunks ahead of their use ----
+  Run put = at;
+  int put_chunk = ch0;
+  const uint8_t* nib = nullptr;   // this lane's 16 bytes of rows lane / 4, + 8, ...
+  const uint8_t* scl = nullptr;   // scales of row `lane` (and lane + 32)
+  const int64_t nib8 = (int64_t)8 * rowb, scl32 = (int64_t)32 * G * SB;
+  const int64_t zoff = (int64_t)N * G * 4;  // zeros follow the scales
+  const bool wide = (G & 3) == 0;  // a chunk's scales start on their whole size
+  const uint32_t nib_to = ring + (uint32_t)((lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4));
+  const uint32_t scl_to = ring + Sl::OFF_SCL + (uint32_t)(lane * Sl::SCL);
+  auto open_put = [&]() {
+    while (put.left > 0 && put.nrows == 0) sh.next(put);
+    if (put.left <= 0) return;
+    const uint8_t* wq = c.packed + (int64_t)put.e * c.expert_bytes;
+    const int64_t row = put.r0 + put.base;
+    nib = wq + (row + (lane >> 2)) * rowb + ch0 * (KC / 2) + (lane & 3) * 16;
+    scl = wq + (int64_t)N * rowb + ((row + lane) * G + 4 * ch0) * SB;
+    put_chunk = ch0;
   };
-  // to the first run at or after the cursor's place where this warp has steps
-  auto settle = [&](Cursor& cu) {
-    while (!cu.done && (cu.steps == 0 || ch0 == ch1)) {
-      cu.v += cu.run.rows;
-      open_run(cu);
-    }
-  };
-  auto advance = [&](Cursor& cu) {
-    if (++cu.step < cu.steps) return;
-    cu.step = 0;
-    if (++cu.chunk < ch1) return;
-    cu.v += cu.run.rows;
-    open_run(cu);
-    settle(cu);
-  };
-
-  auto issue = [&](const Cursor& cu, int slot) {
-    if (!cu.done) {
-      const uint8_t* wq = c.packed + (int64_t)cu.run.e * c.expert_bytes;
-      const int row0 = cu.run.r0 + cu.base + SR * cu.step;  // weight row of the step's first
-      const int nr = min(SR, cu.nrows - SR * cu.step);
-      const int groups = min(4, G - 4 * cu.chunk);          // 4, or 2 at the end of K
-      const uint32_t dst = ring + (uint32_t)(slot * St::BYTES);
-      const uint8_t* nib = wq + (int64_t)row0 * (K >> 1) + (int64_t)cu.chunk * (KC / 2);
-#pragma unroll
-      for (int i = 0; i < SR * 4 / 32; ++i) {
-        const int r = (lane >> 2) + 8 * i, q = lane & 3;
-        if (r < nr && q < groups) cp16(dst + r * NIB_PITCH + q * 16, nib + (int64_t)r * (K >> 1) + q * 16);
+  // scales of one row and chunk: 4 groups, or 2 at the end of K
+  auto copy_scales = [&](uint32_t d, const uint8_t* s, bool half) {
+    if constexpr (FMT == QG_W4_BF16) {
+      if (wide) {
+        cp8(d, s);
+      } else {
+        cp4(d, s);
+        if (!half) cp4(d + 4, s + 4);
       }
-      const uint8_t* scl = wq + (int64_t)N * (K >> 1);
-      if (lane < nr) {
-        const int64_t at = (int64_t)(row0 + lane) * G + 4 * cu.chunk;
-        const uint32_t d = dst + St::OFF_SCL + lane * St::SCL;
-        if constexpr (FMT == QG_W4_BF16) {
-          cp4(d, scl + 2 * at);
-          if (groups == 4) cp4(d + 4, scl + 2 * at + 4);
-        } else {
-          cp8(d, scl + 4 * at);
-          if (groups == 4) cp8(d + 8, scl + 4 * at + 8);
+    } else {
+      if (wide) {
+        cp16(d, s);
+      } else {
+        cp8(d, s);
+        if (!half) cp8(d + 8, s + 8);
+      }
+    }
+  };
+  auto issue = [&](int slot) {
+    if (put.left > 0) {
+      const uint32_t so = (uint32_t)(slot * Sl::BYTES);
+      const bool half = 4 * put_chunk + 4 > G;  // the last 64 of K
+      if (!half || (lane & 3) < 2) {
+        const uint8_t* p = nib;
+#pragma unroll
+        for (int i = 0; i < WROWS / 8; ++i) {
+          if ((lane >> 2) + 8 * i < put.nrows) cp16(nib_to + so + i * 512, p);
+          p += nib8;
         }
-        if constexpr (FMT == QG_W4_ASYM) {
-          const uint8_t* zer = scl + (int64_t)N * G * 4;
-          cp8(dst + St::OFF_ZERO + lane * 16, zer + 4 * at);
-          if (groups == 4) cp8(dst + St::OFF_ZERO + lane * 16 + 8, zer + 4 * at + 8);
+      }
+#pragma unroll
+      for (int i = 0; i < WROWS / 32; ++i) {
+        if (lane + 32 * i < put.nrows) {
+          copy_scales(scl_to + so + i * 32 * Sl::SCL, scl + i * scl32, half);
+          if constexpr (FMT == QG_W4_ASYM)
+            copy_scales(scl_to + so + WROWS * 16 + i * 32 * Sl::SCL, scl + i * scl32 + zoff, half);
         }
+      }
+      nib += KC / 2;
+      scl += 4 * SB;
+      if (++put_chunk == ch1) {
+        sh.next(put);
+        open_put();
       }
     }
     cp_commit();
   };
+  // Thread 0 asks for whole runs in L2, two runs ahead of their use, so that
+  // the ring's loads only have L2's latency to cover.
+  Run ahead = at;
+  bool cold = true;
 
-  Cursor put;
-  put.v = v0;
-  put.done = false;
-  open_run(put);
-  settle(put);
+  if (DENSE) prefetch_x(c);
+  open_put();
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) {
-    issue(put, d);
-    if (!put.done) advance(put);
-  }
-  if (!c.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int d = 0; d < D - 1; ++d) issue(d);
+  if (DENSE) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // every warp walks every run: its steps, then the sum over the K warps
-  Cursor at;
-  at.v = v0;
-  at.done = false;
-  open_run(at);
+  // ldmatrix source of this lane: blocks (rows 0-7, q), (8-15, q), (0-7, q+1), (8-15, q+1)
+  const uint32_t a_at = ring + (uint32_t)(((lane & 15) * 64) + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4));
+  const uint32_t s_at = ring + Sl::OFF_SCL + (uint32_t)(g * Sl::SCL);
+
+  // every warp walks every run: its chunks, then the sum over the K warps
   int slot = 0;
-  while (!at.done) {
-    float acc[2 * RP][NT][4];
+  while (at.left > 0) {
+    const int p0 = sh.tokens_from(at), np = sh.tokens(at);
+    float acc[RT][NT][4];
 #pragma unroll
-    for (int i = 0; i < 2 * RP; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[i][n][k] = 0.0f;
-    // this lane's token rows (MMA column g); columns past the last token
-    // repeat it, and are not stored
-    const uint16_t* xr[NT];
+    if (at.nrows > 0) {
+      // this lane's token rows (MMA column g); columns past the last token
+      // repeat it, and are not stored
+      const uint16_t* xr[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int p = at.run.p0 + min(8 * n + g, at.run.np - 1);
-      int64_t row = p;
-      if (c.src) {
-        const int s = c.src[p];
-        row = s < 0 ? -1 : s / c.topk;
+      for (int n = 0; n < NT; ++n) {
+        const int row = sh.input_row(p0 + min(8 * n + g, np - 1), status);
+        xr[n] = row < 0 ? nullptr : c.in + row * c.ld_in + t * 8;
       }
-      if (row < 0 || row >= c.in_rows) {  // read as zeros
-        record_error(status, QG_ERR_INVALID_ARG);
-        xr[n] = nullptr;
-      } else {
-        xr[n] = c.in + row * c.ld_in;
-      }
-    }
-    if (at.steps > 0) {
+      // B fragments: lane t gives x[8t .. 8t+7] of its group, as A's words do
+      uint4 xb[NT][4], xn[NT][4];
+      auto load_x = [&](uint4 (&x)[NT][4], int ch) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            x[n][q] = make_uint4(0, 0, 0, 0);
+            if (xr[n] && 4 * ch + q < G)
+              x[n][q] = *reinterpret_cast<const uint4*>(xr[n] + (int64_t)ch * KC + q * 32);
+          }
+      };
+      // one block of tokens: the next chunk is read ahead; more of them have
+      // no registers left for that
+      load_x(NT == 1 ? xn : xb, ch0);
       for (int ch = ch0; ch < ch1; ++ch) {
-        const int groups = min(4, G - 4 * ch);
-        uint4 xb[NT][4];
+        const bool half = 4 * ch + 4 > G;  // x is 0 for groups 2 and 3
+        if (NT == 1) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) xb[0][q] = xn[0][q];
+          if (ch + 1 < ch1) load_x(xn, ch + 1);
+        } else if (ch > ch0) {
+          load_x(xb, ch);
+        }
+        // -136 X of this lane's tokens 2t, 2t + 1
+        float z[NT][4][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            xb[n][q] = make_uint4(0, 0, 0, 0);
-            if (xr[n] && q < groups)
-              xb[n][q] = *reinterpret_cast<const uint4*>(xr[n] + (int64_t)ch * KC + q * 32 + t * 8);
+            constexpr uint32_t m = 0xC308C308u;  // -136, -136
+            float d[4];
+            mma16816(d, m, m, m, m, xb[n][q].x, xb[n][q].y, 0.0f, 0.0f);
+            mma16816(d, m, m, m, m, xb[n][q].z, xb[n][q].w);
+            z[n][q][0] = d[0];
+            z[n][q][1] = d[1];
           }
-        // pairs in the order of codes8
+        // The run and the next one into L2, once x has landed (its sums are
+        // finite or not: the test only makes thread 0 wait for them); asked
+        // for earlier, they keep x waiting behind them.
+        if (cold && threadIdx.x == 0 && z[0][0][0] != 12345.678f) {
+          sh.prefetch(ahead, SB, zoff, FMT == QG_W4_ASYM);
+          sh.prefetch(ahead, SB, zoff, FMT == QG_W4_ASYM);
+        }
+        cold = false;
+        issue(slot ^ 1);
+        cp_wait<D - 1>();
+        __syncwarp();
+        const uint32_t so = (uint32_t)(slot * Sl::BYTES);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < RT; ++i) {
+          if (16 * i >= at.nrows) break;
+          uint32_t w01[4], w23[4];  // words of groups 0, 1 and 2, 3: rows g, g + 8 each
+          ldsm4(a_at + so + i * 1024, w01);
+          ldsm4((a_at ^ 32u) + so + i * 1024, w23);
+          float sa[4], sb[4], za[4], zb[4];
+          const uint32_t sc = s_at + so + i * 16 * Sl::SCL;
+          if constexpr (FMT == QG_W4_BF16) {
+            const uint2 u = lds64(sc), v = lds64(sc + 8 * Sl::SCL);
+            sa[0] = __uint_as_float(u.x << 16); sa[1] = __uint_as_float(u.x & 0xFFFF0000u);
+            sa[2] = __uint_as_float(u.y << 16); sa[3] = __uint_as_float(u.y & 0xFFFF0000u);
+            sb[0] = __uint_as_float(v.x << 16); sb[1] = __uint_as_float(v.x & 0xFFFF0000u);
+            sb[2] = __uint_as_float(v.y << 16); sb[3] = __uint_as_float(v.y & 0xFFFF0000u);
+          } else {
+            const float4 u = lds128f(sc), v = lds128f(sc + 8 * Sl::SCL);
+            sa[0] = u.x; sa[1] = u.y; sa[2] = u.z; sa[3] = u.w;
+            sb[0] = v.x; sb[1] = v.y; sb[2] = v.z; sb[3] = v.w;
+          }
+          if constexpr (FMT == QG_W4_ASYM) {
+            const float4 u = lds128f(sc + WROWS * 16), v = lds128f(sc + WROWS * 16 + 8 * 16);
+            const float f = -1.0f / 136.0f;
+            za[0] = f * u.x; za[1] = f * u.y; za[2] = f * u.z; za[3] = f * u.w;
+            zb[0] = f * v.x; zb[1] = f * v.y; zb[2] = f * v.z; zb[3] = f * v.w;
+          }
+          if (half) {  // nothing was copied there
+            sa[2] = sa[3] = sb[2] = sb[3] = 0.0f;
+            if constexpr (FMT == QG_W4_ASYM) za[2] = za[3] = zb[2] = zb[3] = 0.0f;
+          }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint4 v = xb[n][q];
-            xb[n][q] = make_uint4(prmt(v.x, v.y, 0x5410), prmt(v.z, v.w, 0x5410),
-                                  prmt(v.x, v.y, 0x7632), prmt(v.z, v.w, 0x7632));
-          }
+            uint32_t pa[4], pb[4];
+            codes8(q < 2 ? w01[2 * q] : w23[2 * q - 4], pa);
+            codes8(q < 2 ? w01[2 * q + 1] : w23[2 * q - 3], pb);
 #pragma unroll
-        for (int s = 0; s < RP; ++s) {
-          if (s >= at.steps) break;
-          issue(put, slot == 0 ? D - 1 : slot - 1);
-          if (!put.done) advance(put);
-          cp_wait<D - 1>();
-          __syncwarp();
-          const uint32_t st = ring + (uint32_t)(slot * St::BYTES);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (SR * s + 16 * i >= at.nrows) break;
-            const uint32_t ra = st + (16 * i + g) * NIB_PITCH + t * 4;
-            float sa[4], sb[4], za[4], zb[4];
-            const uint32_t sc = st + St::OFF_SCL + (16 * i + g) * St::SCL;
-            if constexpr (FMT == QG_W4_BF16) {
-              const uint2 u = lds64(sc), v = lds64(sc + 8 * St::SCL);
-              sa[0] = __uint_as_float(u.x << 16); sa[1] = __uint_as_float(u.x & 0xFFFF0000u);
-              sa[2] = __uint_as_float(u.y << 16); sa[3] = __uint_as_float(u.y & 0xFFFF0000u);
-              sb[0] = __uint_as_float(v.x << 16); sb[1] = __uint_as_float(v.x & 0xFFFF0000u);
-              sb[2] = __uint_as_float(v.y << 16); sb[3] = __uint_as_float(v.y & 0xFFFF0000u);
-            } else {
-              const float4 u = lds128f(sc), v = lds128f(sc + 8 * St::SCL);
-              sa[0] = u.x; sa[1] = u.y; sa[2] = u.z; sa[3] = u.w;
-              sb[0] = v.x; sb[1] = v.y; sb[2] = v.z; sb[3] = v.w;
-            }
-            if constexpr (FMT == QG_W4_ASYM) {
-              const uint32_t zc = st + St::OFF_ZERO + (16 * i + g) * 16;
-              const float4 u = lds128f(zc), v = lds128f(zc + 8 * 16);
-              za[0] = u.x; za[1] = u.y; za[2] = u.z; za[3] = u.w;
-              zb[0] = v.x; zb[1] = v.y; zb[2] = v.z; zb[3] = v.w;
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (q >= groups) break;
-              uint32_t pa[4], pb[4];
-              codes8(lds32(ra + q * 16), pa);
-              codes8(lds32(ra + 8 * NIB_PITCH + q * 16), pb);
-              const uint32_t a0[4] = {pa[0], pb[0], pa[1], pb[1]};
-              const uint32_t a1[4] = {pa[2], pb[2], pa[3], pb[3]};
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma16816(d, a0, xb[n][q].x, xb[n][q].y);
-                mma16816(d, a1, xb[n][q].z, xb[n][q].w);
-                float* ac = acc[2 * s + i][n];
-                ac[0] = fmaf(sa[q], d[0], ac[0]);
-                ac[1] = fmaf(sa[q], d[1], ac[1]);
-                ac[2] = fmaf(sb[q], d[2], ac[2]);
-                ac[3] = fmaf(sb[q], d[3], ac[3]);
-                if constexpr (FMT == QG_W4_ASYM) {
-                  // X[p,g] in every row: MMAs with ones
-                  const uint32_t one[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-                  float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                  mma16816(x, one, xb[n][q].x, xb[n][q].y);
-                  mma16816(x, one, xb[n][q].z, xb[n][q].w);
-                  ac[0] = fmaf(za[q], x[0], ac[0]);
-                  ac[1] = fmaf(za[q], x[1], ac[1]);
-                  ac[2] = fmaf(zb[q], x[2], ac[2]);
-                  ac[3] = fmaf(zb[q], x[3], ac[3]);
-                }
+            for (int n = 0; n < NT; ++n) {
+              float d[4];
+              mma16816(d, pa[0], pb[0], pa[1], pb[1], xb[n][q].x, xb[n][q].y, z[n][q][0], z[n][q][1]);
+              mma16816(d, pa[2], pb[2], pa[3], pb[3], xb[n][q].z, xb[n][q].w);
+              float* ac = acc[i][n];
+              ac[0] = fmaf(sa[q], d[0], ac[0]);
+              ac[1] = fmaf(sa[q], d[1], ac[1]);
+              ac[2] = fmaf(sb[q], d[2], ac[2]);
+              ac[3] = fmaf(sb[q], d[3], ac[3]);
+              if constexpr (FMT == QG_W4_ASYM) {
+                ac[0] = fmaf(za[q], z[n][q][0], ac[0]);
+                ac[1] = fmaf(za[q], z[n][q][1], ac[1]);
+                ac[2] = fmaf(zb[q], z[n][q][0], ac[2]);
+                ac[3] = fmaf(zb[q], z[n][q][1], ac[3]);
               }
             }
           }
-          __syncwarp();  // the slot may be filled again
-          slot = slot + 1 == D ? 0 : slot + 1;
         }
+        __syncwarp();  // the slot may be filled again
+        slot ^= 1;
       }
-    }
-    // partial sums [K warp][token][row]; a lane holds rows g, g + 8 and
-    // columns 2t, 2t + 1 of each tile
-    if (at.steps > 0) {
+      // partial sums [K warp][token][row]; a lane holds rows g, g + 8 and
+      // columns 2t, 2t + 1 of each tile
 #pragma unroll
-      for (int i = 0; i < 2 * RP; ++i) {
+      for (int i = 0; i < RT; ++i) {
         if (16 * i >= at.nrows) break;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -409,41 +564,34 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1)
         }
       }
     }
+    if (threadIdx.x == 0) sh.prefetch(ahead, SB, zoff, FMT == QG_W4_ASYM);
     __syncthreads();
-    for (int o = threadIdx.x; o < at.run.rows * at.run.np; o += W * 32) {
-      const int tok = o / at.run.rows, r = o - tok * at.run.rows;
-      float s = 0.0f;
-      for (int k = 0; k < wk; ++k) s += part[((size_t)k * 8 * NT + tok) * prows + r];
-      const int n = at.run.r0 + r;
-      if (c.bias) s += __ldg(c.bias + (int64_t)at.run.e * N + n);
-      c.out[(int64_t)(at.run.p0 + tok) * c.ld_out + n] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
-    }
+    sum_and_store(c, at, p0, np, 8 * NT, wk, part, prows);
     __syncthreads();
-    at.v += at.run.rows;
-    open_run(at);
+    sh.next(at);
   }
   cp_wait<0>();
 }
 
-template <int FMT, int NT>
-struct Ring {
-  static constexpr int D = 3;
-};
-
-size_t rows_smem(int fmt, int nt, int d, int wk, int E) {
-  const int step = fmt == QG_W4_BF16 ? Step<QG_W4_BF16>::BYTES
-                   : fmt == QG_W4_F32 ? Step<QG_W4_F32>::BYTES : Step<QG_W4_ASYM>::BYTES;
-  return (size_t)W * d * step + (size_t)wk * 8 * nt * (WROWS * (W / wk) + 4) * 4 +
+size_t rows_smem(int fmt, int nt, int wk, int E) {
+  const int slot = fmt == QG_W4_BF16 ? Slot<QG_W4_BF16>::BYTES
+                   : fmt == QG_W4_F32 ? Slot<QG_W4_F32>::BYTES : Slot<QG_W4_ASYM>::BYTES;
+  return (size_t)W * D * slot + (size_t)wk * 8 * nt * (WROWS * (W / wk) + 4) * 4 +
          (size_t)(3 * E + 1) * 4;
 }
 
-template <int FMT, int NT>
-int run_rows(const RowsArgs& a, cudaStream_t st) {
-  constexpr int D = Ring<FMT, NT>::D;
-  const size_t smem = rows_smem(FMT, NT, D, a.wk, a.c.E);
-  const int per_sm = smem <= 112 * 1024 ? 2 : 1;
+template <int FMT, int NT, bool DENSE>
+int run_rows(RowsArgs a, cudaStream_t st) {
+  const size_t smem = rows_smem(FMT, NT, a.wk, a.c.E);
+  int ctas = num_sms() * (NT <= 2 && smem <= 113 * 1024 ? 2 : 1);
+  if (DENSE) {  // in blocks of 8 rows, half an MMA tile
+    const int blocks = (int)cdiv(a.c.N, 8);
+    ctas = (int)min64(ctas, blocks);
+    a.share = blocks / ctas;
+    a.more = blocks % ctas;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(num_sms() * per_sm));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(W * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -452,33 +600,45 @@ int run_rows(const RowsArgs& a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, a16w4_rows_kernel<FMT, NT, D>, a, status_word()) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, a16w4_rows_kernel<FMT, NT, DENSE>, a, status_word()) == cudaSuccess
              ? QG_OK
              : QG_ERR_CUDA;
 }
 
 template <int FMT>
 int run_rows_nt(int nt, const RowsArgs& a, cudaStream_t st) {
-  if (nt == 1) return run_rows<FMT, 1>(a, st);
-  if (nt == 2) return run_rows<FMT, 2>(a, st);
-  return run_rows<FMT, 4>(a, st);
+  if (!a.c.offsets) {
+    if (nt == 1) return run_rows<FMT, 1, true>(a, st);
+    if (nt == 2) return run_rows<FMT, 2, true>(a, st);
+    return run_rows<FMT, 4, true>(a, st);
+  }
+  if (nt == 1) return run_rows<FMT, 1, false>(a, st);
+  if (nt == 2) return run_rows<FMT, 2, false>(a, st);
+  return run_rows<FMT, 4, false>(a, st);
 }
 
-template <int FMT, int NT>
+template <int FMT, int NT, bool DENSE>
 int set_rows_smem() {
-  const size_t most = rows_smem(FMT, NT, Ring<FMT, NT>::D, W, kA16W4MaxExperts);
-  return cudaFuncSetAttribute((const void*)a16w4_rows_kernel<FMT, NT, Ring<FMT, NT>::D>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)most) == cudaSuccess
+  size_t most = 0;
+  for (int wk = 1; wk <= W; wk *= 2) {
+    const size_t b = rows_smem(FMT, NT, wk, kA16W4MaxExperts);
+    most = b > most ? b : most;
+  }
+  return cudaFuncSetAttribute((const void*)a16w4_rows_kernel<FMT, NT, DENSE>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) ==
+                 cudaSuccess
              ? QG_OK
              : QG_ERR_CUDA;
 }
 
 template <int FMT>
 int set_rows_smem_nt() {
-  int rc = set_rows_smem<FMT, 1>();
-  if (rc == QG_OK) rc = set_rows_smem<FMT, 2>();
-  if (rc == QG_OK) rc = set_rows_smem<FMT, 4>();
+  int rc = set_rows_smem<FMT, 1, true>();
+  if (rc == QG_OK) rc = set_rows_smem<FMT, 2, true>();
+  if (rc == QG_OK) rc = set_rows_smem<FMT, 4, true>();
+  if (rc == QG_OK) rc = set_rows_smem<FMT, 1, false>();
+  if (rc == QG_OK) rc = set_rows_smem<FMT, 2, false>();
+  if (rc == QG_OK) rc = set_rows_smem<FMT, 4, false>();
   return rc;
 }
 
@@ -498,8 +658,7 @@ int launch_a16w4_rows(const A16W4Call& c, cudaStream_t st) {
   a.chunks = (int)cdiv(c.K, KC);
   a.wk = 1;
   while (a.wk * 2 <= W && a.wk * 2 <= a.chunks) a.wk *= 2;
-  a.min_rows = 8;
-  // token rows per pass: what one expert has, as far as the host knows
+  // tokens per pass: what one expert has, as far as the host knows
   const int64_t each = cdiv(c.S, c.E);
   const int nt = each <= 8 ? 1 : each <= 16 ? 2 : 4;
   if (c.format == QG_W4_F32) return run_rows_nt<QG_W4_F32>(nt, a, st);
