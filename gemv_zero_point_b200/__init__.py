@@ -112,8 +112,9 @@ _sig("pack_w4_g32_bf16", _i32, [_i32, _i32, _vp, _i64, _vp, _vp, _sz, _vp])
 _sig("qgemm_a8w4_f32_bf16s", _i32, [_i32, _i32, _i32, _vp, _i64, _vp, _vp, _f32, _f32, _vp,
                                     _i64, _vp, _vp, _vp, _vp, _sz, _vp])
 _sig("qgemm_a16w4_bf16", _i32, [_i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _vp])
+_sig("qgemm_a16w4_bf16_experts_workspace_bytes", _sz, [_i32, _i32, _i32, _i32])
 _sig("qgemm_a16w4_bf16_experts", _i32, [_i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _vp,
-                                        _i64, _i32, _vp, _vp, _i64, _vp])
+                                        _i64, _i32, _vp, _vp, _i64, _vp, _sz, _vp])
 _sig("qgemm_a16w4_bf16_grad_x", _i32, [_i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _vp])
 _sig("qgemm_a16w4_bf16_experts_grad_x", _i32, [_i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i64,
                                                _i32, _vp, _i64, _vp])
@@ -536,7 +537,7 @@ def qgemm_a16w4_bf16(x, packed_w, y, bias=None, weights="f32", stream=None):
 
 
 def qgemm_a16w4_bf16_experts(x, offsets, packed_w, y, src=None, topk=1, bias=None, weights="f32",
-                             stream=None):
+                             workspace=None, stream=None):
     """y[p] = W[e] @ x[src[p] // topk] + bias[e] (x[p] without src) for the rows
     p of expert e, offsets[e] <= p < offsets[e+1]; packed_w uint8 [E][bytes]."""
     torch = _torch()
@@ -549,9 +550,17 @@ def qgemm_a16w4_bf16_experts(x, offsets, packed_w, y, src=None, topk=1, bias=Non
         _check_dense(src, torch.int32, (S,), "src")
     if bias is not None:
         _check_dense(bias, torch.float32, (E, N), "bias")
-    _launch(lib.qgemm_a16w4_bf16_experts, stream, x.get_device(), (offsets, packed_w, y, src, bias),
+    have = 0
+    if workspace is not None:
+        have = workspace.numel() * workspace.element_size()
+    elif src is not None:
+        have = lib.qgemm_a16w4_bf16_experts_workspace_bytes(E, S, K, 1)
+        if have:
+            workspace = _empty_bytes(have, x.device)
+    _launch(lib.qgemm_a16w4_bf16_experts, stream, x.get_device(),
+            (offsets, packed_w, y, src, bias, workspace),
             (E, S, N, K, x.data_ptr(), ldx, rows, _addr(src), topk, offsets.data_ptr(),
-             packed_w.data_ptr(), step, fmt, _addr(bias), y.data_ptr(), ldy))
+             packed_w.data_ptr(), step, fmt, _addr(bias), y.data_ptr(), ldy, _addr(workspace), have))
 
 
 def qgemm_a16w4_bf16_grad_x(dy, packed_w, dx, weights="f32", stream=None):

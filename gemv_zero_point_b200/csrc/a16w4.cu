@@ -682,10 +682,7 @@ int64_t packed_bytes(int N, int K, int format) {
 
 // Few rows per expert stream the weights past warp MMAs, more go to the
 // tensor cores.
-int launch_product(const A16W4Call& c, cudaStream_t st) {
-  if (cdiv(c.S, c.E) <= 32) return launch_a16w4_rows(c, st);
-  return launch_a16w4_tc(c, false, st);
-}
+bool few_rows(int E, int S) { return cdiv(S, E) <= 32; }
 
 // Checks of every product: QG_OK when the call can run (S may be 0).
 int product_args(int E, int S, int N, int K, const void* in, int64_t ld_in, int in_cols,
@@ -722,7 +719,8 @@ extern "C" int qgemm_a16w4_bf16(int M, int N, int K, const void* x, int64_t ldx,
   c.in = (const uint16_t*)x; c.ld_in = ldx; c.in_rows = M; c.topk = 1;
   c.packed = (const uint8_t*)packed_w; c.format = format; c.bias = bias;
   c.out = (uint16_t*)y; c.ld_out = ldy;
-  return launch_product(c, (cudaStream_t)stream);
+  return few_rows(1, M) ? launch_a16w4_rows(c, (cudaStream_t)stream)
+                        : launch_a16w4_tc(c, false, nullptr, (cudaStream_t)stream);
 }
 
 extern "C" int qgemm_a16w4_bf16_grad_x(int M, int N, int K, const void* dy, int64_t lddy,
@@ -737,7 +735,7 @@ extern "C" int qgemm_a16w4_bf16_grad_x(int M, int N, int K, const void* dy, int6
   c.in = (const uint16_t*)dy; c.ld_in = lddy; c.in_rows = M; c.topk = 1;
   c.packed = (const uint8_t*)packed_w; c.format = format;
   c.out = (uint16_t*)dx; c.ld_out = lddx;
-  return launch_a16w4_tc(c, true, (cudaStream_t)stream);
+  return launch_a16w4_tc(c, true, nullptr, (cudaStream_t)stream);
 }
 
 extern "C" int qgemm_a16w4_bf16_experts_grad_x(int E, int S, int N, int K, const void* dy,
@@ -756,20 +754,29 @@ extern "C" int qgemm_a16w4_bf16_experts_grad_x(int E, int S, int N, int K, const
   c.in = (const uint16_t*)dy; c.ld_in = lddy; c.in_rows = S; c.topk = 1;
   c.offsets = offsets; c.packed = (const uint8_t*)packed_w; c.expert_bytes = expert_bytes;
   c.format = format; c.out = (uint16_t*)dx; c.ld_out = lddx;
-  return launch_a16w4_tc(c, true, (cudaStream_t)stream);
+  return launch_a16w4_tc(c, true, nullptr, (cudaStream_t)stream);
+}
+
+extern "C" size_t qgemm_a16w4_bf16_experts_workspace_bytes(int E, int S, int K, int indirect) {
+  if (E <= 0 || S <= 0 || K <= 0 || K % 64) return 0;
+  return few_rows(E, S) ? 0 : a16w4_tc_workspace(S, K, indirect != 0);
 }
 
 extern "C" int qgemm_a16w4_bf16_experts(int E, int S, int N, int K, const void* x, int64_t ldx,
                                         int x_rows, const int32_t* src, int topk,
                                         const int32_t* offsets, const void* packed_w,
                                         int64_t expert_bytes, int format, const float* bias,
-                                        void* y, int64_t ldy, void* stream) {
+                                        void* y, int64_t ldy, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
   int rc = product_args(E, S, N, K, x, ldx, K, packed_w, expert_bytes, format, bias, y, ldy, N);
   if (rc != QG_OK) return rc;
   if (topk <= 0 || x_rows < 0) return QG_ERR_INVALID_ARG;
   if (S == 0) return QG_OK;
   if (!offsets || x_rows == 0 || (!src && x_rows < S)) return QG_ERR_INVALID_ARG;
   if (((uintptr_t)offsets | (uintptr_t)src) & 3) return QG_ERR_MISALIGNED;
+  const size_t need = qgemm_a16w4_bf16_experts_workspace_bytes(E, S, K, src != nullptr);
+  if (need && (!workspace || workspace_bytes < need)) return QG_ERR_WORKSPACE;
+  if (need && ((uintptr_t)workspace & 255)) return QG_ERR_MISALIGNED;
   rc = device_setup_status();
   if (rc != QG_OK) return rc;
   A16W4Call c{};
@@ -777,5 +784,6 @@ extern "C" int qgemm_a16w4_bf16_experts(int E, int S, int N, int K, const void* 
   c.in = (const uint16_t*)x; c.ld_in = ldx; c.in_rows = x_rows; c.src = src; c.topk = topk;
   c.offsets = offsets; c.packed = (const uint8_t*)packed_w; c.expert_bytes = expert_bytes;
   c.format = format; c.bias = bias; c.out = (uint16_t*)y; c.ld_out = ldy;
-  return launch_product(c, (cudaStream_t)stream);
+  return few_rows(E, S) ? launch_a16w4_rows(c, (cudaStream_t)stream)
+                        : launch_a16w4_tc(c, false, workspace, (cudaStream_t)stream);
 }

@@ -28,7 +28,9 @@ struct A16W4Call {
 };
 constexpr int kA16W4MaxExperts = 1024;
 int launch_a16w4_rows(const A16W4Call& c, cudaStream_t st);           // few rows (a16w4.cu)
-int launch_a16w4_tc(const A16W4Call& c, bool grad, cudaStream_t st);  // many rows (a16w4_tc.cu)
+// many rows (a16w4_tc.cu); indirect rows need a workspace to be sorted in
+int launch_a16w4_tc(const A16W4Call& c, bool grad, void* ws, cudaStream_t st);
+size_t a16w4_tc_workspace(int S, int K, bool gather);
 
 // Rows [start, start + count) of expert e; a range that is not inside [0, S)
 // is an error of the caller's: recorded, then no rows.

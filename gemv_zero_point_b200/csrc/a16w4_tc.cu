@@ -4,27 +4,38 @@
 //   forward   y[p,n]  = sum_k x[p,k] * w[n,k] + bias[n]     features n, reduction k
 //   gradient  dx[p,k] = sum_n dy[p,n] * w[n,k]              features k, reduction n
 //
-// One tile is 128 features (MMA M, TMEM lanes) x up to 256 rows (MMA N, TMEM
-// columns): the rows are the side of free size, in steps of 16, so the
-// ragged row counts of experts waste little.  The weights are expanded to
-// bf16 on the way into shared memory: w is formed as the real value and
-// rounded to bf16 once (half a step, 2^-8 of w), the price of one MMA per
-// weight; the sums stay in f32 (TMEM) and the output is rounded once.  With
-// 256 rows a stage's four MMAs take 256 cycles, and the expansion of its 8192
-// weights about 150 issue cycles, so the expansion hides behind the MMAs.
+// One tile is 256 features on a pair of CTAs (cta_group::2: 128 features, MMA
+// M, TMEM lanes, in each) x up to 256 rows (MMA N, TMEM columns): the rows are
+// the side of free size, so the ragged row counts of experts waste little.
+// The weights are expanded to bf16 on the way into shared memory: w is formed
+// as the real value and rounded to bf16 once (half a step, 2^-8 of w), the
+// price of one MMA per weight; the sums stay in f32 (TMEM) and the output is
+// rounded once.
+//
+// What bounds it is shared memory: for 256 rows a 64-wide stage's MMAs take
+// 512 cycles, and a CTA on its own moves 104 KB for them (rows 32 KB in and
+// 32 out, bf16 weights 16 in and 16 out, nibbles 4 and 4), 832 cycles at 128
+// bytes a cycle; it measured 1250.  In a pair each CTA holds half of the rows:
+// 72 KB.  A single CTA remains for calls with few tiles, where pairs would
+// leave SMs without work.
 //
 // Both directions read the same packed matrix.  Forward, a stage is 128 rows
 // n x 64 k of it and the bf16 tile is K-major; for the gradient it is 64 rows
 // n x 128 k and the tile's features (k) run along the rows, so the same
 // row-wise expansion writes an MN-major operand: no transpose anywhere.
 //
-// Roles (512 threads, one CTA per SM, persistent over tiles):
-//   warp 0      rows: tensor copies of 64-wide slices (128-byte swizzle), or
-//               row gathers of four rows each when the rows are indirect
-//   warp 1      TMEM; MMA issue, one commit per stage and one per tile
+// Roles (768 threads, one CTA per SM, persistent over tiles):
+//   warp 0      rows: tensor copies of 64-wide slices (128-byte swizzle)
+//   warp 1      TMEM; MMA issue by one thread (of the pair's first CTA), one
+//               commit per stage and one per tile
 //   warp 2      nibbles: tensor copies, a ring of their own
 //   warps 4-7   epilogue: TMEM -> bf16 -> global, overlapping the next tile
-//   warps 8-15  expansion of the nibbles into the swizzled bf16 stage
+//   warps 8-23  expansion of the nibbles into the swizzled bf16 stage, two
+//               groups of eight warps that take the stages in turn (one stage
+//               takes a group about 700 cycles, mostly latencies)
+// Indirect rows are first brought into sorted order in the workspace (about
+// 45 us for 32768 rows of 2048, next to 260): gathering them here took 963 us
+// in all with tensor-map row gathers of four rows, 534 with cp.async.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -37,24 +48,29 @@ namespace qg {
 
 namespace {
 
-constexpr int TF = 128;                    // features per tile
+constexpr int TF = 128;                    // features per CTA and tile
 constexpr int TT = 256;                    // rows per tile at most
 constexpr int KS = 64;                     // reduction per stage: one 128-byte swizzle row
 constexpr int XBOX = 64;                   // rows per tensor copy
-constexpr int STAGES = 4;
 constexpr int NRING = 6;
-constexpr int X_BYTES = TT * KS * 2;       // 32 KiB
 constexpr int W_BYTES = TF * KS * 2;       // 16 KiB
 constexpr int NIB_BYTES = TF * KS / 2;     // 4 KiB
-constexpr int THREADS = 512;
-constexpr int EPI_WARP0 = 4, CONV_WARP0 = 8, CONV_WARPS = 8;
+constexpr int THREADS = 768;
+constexpr int EPI_WARP0 = 4, CONV_WARP0 = 8, CONV_WARPS = 8;  // CONV_WARPS per group
 
-constexpr size_t OFF_X = 0;
-constexpr size_t OFF_W = OFF_X + (size_t)STAGES * X_BYTES;
-constexpr size_t OFF_N = OFF_W + (size_t)STAGES * W_BYTES;
-constexpr size_t OFF_BAR = OFF_N + (size_t)NRING * NIB_BYTES;
-constexpr size_t OFF_PRE = OFF_BAR + 512;
-size_t tc_smem(int E) { return 1024 + OFF_PRE + (size_t)(E + 1) * 4; }
+template <bool PAIR>
+struct Lay {
+  static constexpr int X_BYTES = (PAIR ? TT / 2 : TT) * KS * 2;  // rows of this CTA
+  static constexpr int STAGES = PAIR ? 6 : 4;
+  static constexpr size_t OFF_W = (size_t)STAGES * X_BYTES;
+  static constexpr size_t OFF_N = OFF_W + (size_t)STAGES * W_BYTES;
+  static constexpr size_t OFF_BAR = OFF_N + (size_t)NRING * NIB_BYTES;
+  static constexpr size_t OFF_PRE = OFF_BAR + 512;
+};
+template <bool PAIR>
+size_t tc_smem(int E) {
+  return 1024 + Lay<PAIR>::OFF_PRE + (size_t)(E + 1) * 4;
+}
 
 struct TcMaps {
   CUtensorMap nib, rows;
@@ -81,12 +97,51 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
   return d;
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                         uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+// Arrive on `bar` (in both CTAs of a pair) once the MMAs issued so far end.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (PAIR) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)0x3)
+        : "memory");
+  } else {
+    mma_commit(bar);
+  }
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+// Tensor load that completes on the barrier at cluster address `bar`, which
+// may be the other CTA's (no multicast).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int x, int y,
+                                                 uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 
@@ -99,18 +154,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
-// Four rows r.x .. r.w of a one-row box; rows outside the tensor read as zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int x, int4 r,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Every lane waits; the warp takes its decision together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status) {
+  // a phase that is complete is seen at once; a parked wait costs about 180
+  // cycles even then
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_park(bar, parity, status));
 }
 
@@ -145,17 +193,17 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
   return d;
 }
 
-// Raw stored values of group `at`: loaded ahead, turned into a Scale at use.
+// Raw stored scale (and zero, zoff bytes further): loaded ahead, turned into
+// a Scale at use.
 template <int FMT>
-__device__ __forceinline__ uint2 load_scale(const uint8_t* scl, const uint8_t* zer, int64_t at,
-                                            bool in) {
+__device__ __forceinline__ uint2 load_scale(const uint8_t* p, int64_t zoff, bool in) {
   uint2 v = make_uint2(0, 0);
   if (in) {
     if constexpr (FMT == QG_W4_BF16) {
-      v.x = __ldg(reinterpret_cast<const unsigned short*>(scl) + at);
+      v.x = __ldg(reinterpret_cast<const unsigned short*>(p));
     } else {
-      v.x = __ldg(reinterpret_cast<const uint32_t*>(scl) + at);
-      if constexpr (FMT == QG_W4_ASYM) v.y = __ldg(reinterpret_cast<const uint32_t*>(zer) + at);
+      v.x = __ldg(reinterpret_cast<const uint32_t*>(p));
+      if constexpr (FMT == QG_W4_ASYM) v.y = __ldg(reinterpret_cast<const uint32_t*>(p + zoff));
     }
   }
   return v;
@@ -206,33 +254,35 @@ __device__ __forceinline__ void expand8(uint32_t w, const Scale<FMT>& s, uint32_
   }
 }
 
-template <int FMT, bool GRAD, bool GATHER>
+template <int FMT, bool GRAD, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     a16w4_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a,
                     int* status) {
+  using L = Lay<PAIR>;
+  constexpr int STAGES = L::STAGES, X_BYTES = L::X_BYTES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  const uint32_t sX = smem_u32(smem + OFF_X), sW = smem_u32(smem + OFF_W);
-  const uint32_t sN = smem_u32(smem + OFF_N);
-  uint64_t* x_full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-  uint64_t* w_full = x_full + STAGES;
-  uint64_t* empty = w_full + STAGES;
+  const uint32_t sX = smem_u32(smem), sW = smem_u32(smem + L::OFF_W);
+  const uint32_t sN = smem_u32(smem + L::OFF_N);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);  // rows and weights of a stage
+  uint64_t* empty = full + STAGES;
   uint64_t* n_full = empty + STAGES;
   uint64_t* n_empty = n_full + NRING;
   uint64_t* t_full = n_empty + NRING;
   uint64_t* t_empty = t_full + 2;
   uint64_t* drain = t_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  int* pre = reinterpret_cast<int*>(smem + OFF_PRE);  // [E + 1] row tiles before expert e
+  int* pre = reinterpret_cast<int*>(smem + L::OFF_PRE);  // [E + 1] row tiles before expert e
 
   const A16W4Call& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0;  // rank 0 issues the pair's MMAs
+  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&x_full[s], 1);
-      mbar_init(&w_full[s], CONV_WARPS);
+      mbar_init(&full[s], 1 + (PAIR ? 2 * CONV_WARPS : CONV_WARPS));
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < NRING; ++s) {
@@ -241,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&t_full[b], 1);
-      mbar_init(&t_empty[b], 4);
+      mbar_init(&t_empty[b], PAIR ? 8 : 4);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -249,11 +299,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     prefetch_tmap(&maps.rows);
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(tmem_slot)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(tmem_slot)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(tmem_slot)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   // the offsets come from the work before this call
   if (c.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -276,17 +334,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) pre[c.E] = carry;
   }
   tc_fence_before();
-  __syncthreads();
+  // in a pair, both CTAs' barriers exist before any signal between them
+  if constexpr (PAIR) cluster_sync_all(); else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int64_t total = (int64_t)pre[c.E] * a.ftiles;
   const int stages = a.stages;
 
+  constexpr int kRowStep = PAIR ? 32 : 16;  // MMA N in steps of 16 per CTA
   // tile t: features fastest, so concurrent CTAs share the rows' tiles
   auto tile_at = [&](int64_t t) {
     Tile r;
     const int u = (int)(t / a.ftiles);
-    r.f0 = (int)(t - (int64_t)u * a.ftiles) * TF;
+    r.f0 = (int)(t - (int64_t)u * a.ftiles) * (PAIR ? 2 * TF : TF) + (int)rank * TF;
     int lo = 0, hi = c.E - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -296,7 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int2 range = expert_range(c.offsets, lo, c.S, nullptr);
     // an expert's rows in equal tiles
     const int nt = pre[lo + 1] - pre[lo];
-    const int per = ((range.y + nt - 1) / nt + 15) & ~15;
+    const int per = ((range.y + nt - 1) / nt + kRowStep - 1) & ~(kRowStep - 1);
     const int from = min((u - pre[lo]) * per, range.y);
     r.p0 = range.x + from;
     r.np = min(per, range.y - from);
@@ -304,57 +364,43 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp == 0) {
-    // ---------------- rows ----------------
+    // ---------------- rows: this CTA's half, or all ----------------
     asm volatile("griddepcontrol.wait;" ::: "memory");
     uint32_t it = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
-      int4 r0, r1;  // GATHER: input rows of tile rows 8*lane .. 8*lane + 7
-      uint32_t bytes = (uint32_t)((tl.np + XBOX - 1) / XBOX) * (XBOX * KS * 2);
-      if constexpr (GATHER) {
-        int rr[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = 8 * lane + i;
-          rr[i] = c.in_rows;  // outside: zeros
-          if (j < tl.np) {
-            const int s = c.src[tl.p0 + j];
-            const int q = s < 0 ? c.in_rows : s / c.topk;
-            if (q >= c.in_rows) record_error(status, QG_ERR_INVALID_ARG);
-            else rr[i] = q;
-          }
-        }
-        r0 = make_int4(rr[0], rr[1], rr[2], rr[3]);
-        r1 = make_int4(rr[4], rr[5], rr[6], rr[7]);
-        bytes = (uint32_t)((tl.np + 3) / 4) * (4 * KS * 2);
-      }
+      const int n = (tl.np + kRowStep - 1) & ~(kRowStep - 1);
+      const int mine = PAIR ? n / 2 : n;
+      const int y = tl.p0 + (int)rank * mine;
+      const int boxes = (mine + XBOX - 1) / XBOX;
       for (int s = 0; s < stages; ++s, ++it) {
         const int slot = it % STAGES;
         if (it >= STAGES) ok = warp_wait(&empty[slot], ((it / STAGES) - 1) & 1, status);
         if (!ok) break;
-        const uint32_t dst = sX + slot * X_BYTES;
-        if (lane == 0) mbar_arrive_expect_tx(&x_full[slot], bytes);
+        if (lane == 0 && rank == 0)
+          mbar_arrive_expect_tx(&full[slot], (uint32_t)boxes * (XBOX * KS * 2) * (PAIR ? 2u : 1u));
         __syncwarp();
-        if constexpr (GATHER) {
-          if (8 * lane < tl.np) tma_gather4(dst + lane * 1024, &maps.rows, s * KS, r0, &x_full[slot]);
-          if (8 * lane + 4 < tl.np)
-            tma_gather4(dst + lane * 1024 + 512, &maps.rows, s * KS, r1, &x_full[slot]);
-        } else {
-          if (lane * XBOX < tl.np)
-            tma_load_2d(smem + OFF_X + slot * X_BYTES + lane * (XBOX * KS * 2), &maps.rows, s * KS,
-                        tl.p0 + lane * XBOX, &x_full[slot]);
+        if (lane < boxes) {
+          const uint32_t dst = sX + slot * X_BYTES + lane * (XBOX * KS * 2);
+          if constexpr (PAIR)
+            tma_load_2d_pair(dst, &maps.rows, s * KS, y + lane * XBOX, mapa(smem_u32(&full[slot]), 0));
+          else
+            tma_load_2d(smem + slot * X_BYTES + lane * (XBOX * KS * 2), &maps.rows, s * KS,
+                        y + lane * XBOX, &full[slot]);
         }
       }
     }
-    // every copy has landed before the CTA may exit
-    for (uint32_t k = it > STAGES ? it - STAGES : 0; k < it; ++k)
-      warp_wait(&x_full[k % STAGES], (k / STAGES) & 1, status);
+    // every copy has landed before the CTA may exit (in a pair the first CTA
+    // waits for both, and the CTAs end together)
+    if (rank == 0)
+      for (uint32_t k = it > STAGES ? it - STAGES : 0; k < it; ++k)
+        warp_wait(&full[k % STAGES], (k / STAGES) & 1, status);
   } else if (warp == 2) {
     // ---------------- nibbles (inputs of the call alone) ----------------
     uint32_t it = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
       for (int s = 0; s < stages; ++s, ++it) {
         const int slot = it % NRING;
@@ -372,99 +418,125 @@ __global__ void __launch_bounds__(THREADS, 1)
       warp_wait(&n_full[k % NRING], (k / NRING) & 1, status);
   } else if (warp == 1) {
     // ---------------- MMA issue ----------------
-    uint32_t it = 0, use = 0;
-    bool ok = true;
-    for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x, ++use) {
-      const Tile tl = tile_at(t);
-      const int n = (tl.np + 15) & ~15;
-      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (GRAD ? 1u << 15 : 0u) |
-                             ((uint32_t)(n >> 3) << 17) | ((uint32_t)(TF >> 4) << 24);
-      const uint32_t buf = use & 1;
-      ok = warp_wait(&t_empty[buf], ((use >> 1) & 1) ^ 1, status);
-      if (!ok) break;
-      const uint32_t d = tmem_base + buf * TT;
-      for (int s = 0; s < stages; ++s, ++it) {
-        const int slot = it % STAGES;
-        const uint32_t par = (it / STAGES) & 1;
-        ok = warp_wait(&x_full[slot], par, status) && warp_wait(&w_full[slot], par, status);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t dx = sdesc_sw128(sX + slot * X_BYTES);
-          const uint64_t dw = GRAD ? sdesc_mn_sw128(sW + slot * W_BYTES) : sdesc_sw128(sW + slot * W_BYTES);
-          // descriptor addresses count 16 bytes: 16 k further is 32 bytes of
-          // a K-major row, or 16 rows of 128 bytes of the MN-major tile
+    // One thread, and every stage passes through it: with divisions by the
+    // ring's size, two barriers a stage and polled waits it took 1050 cycles a
+    // stage, twice the MMAs' own time.
+    if (lane == 0 && rank == 0) {
+      uint32_t use = 0, slot = 0, par = 0;
+      bool ok = true;
+      const uint64_t dx0 = sdesc_sw128(sX), dw0 = GRAD ? sdesc_mn_sw128(sW) : sdesc_sw128(sW);
+      uint64_t dx = dx0, dw = dw0;  // of the slot; descriptor addresses count 16 bytes
+      for (int64_t t = first; t < total && ok; t += step, ++use) {
+        const Tile tl = tile_at(t);
+        const int n = (tl.np + kRowStep - 1) & ~(kRowStep - 1);
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (GRAD ? 1u << 15 : 0u) |
+                               ((uint32_t)(n >> 3) << 17) |
+                               ((uint32_t)((PAIR ? 2 * TF : TF) >> 4) << 24);
+        const uint32_t buf = use & 1;
+        ok = mbar_wait(&t_empty[buf], ((use >> 1) & 1) ^ 1, status);
+        const uint32_t d = tmem_base + buf * TT;
+        uint32_t more = 0;  // the tile's first MMA overwrites
+        for (int s = 0; s < stages && ok; ++s) {
+          ok = mbar_wait(&full[slot], par, status);
+          if (!ok) break;
+          tc_fence_after();
+          // 16 k further is 32 bytes of a K-major row, or 16 rows of 128
+          // bytes of the MN-major tile
+          mma_f16<PAIR>(d, dw, dx, idesc, more);
 #pragma unroll
-          for (int k = 0; k < KS / 16; ++k)
-            mma_f16(d, dw + (GRAD ? 128 : 2) * k, dx + 2 * k, idesc, s > 0 || k > 0);
-          mma_commit(&empty[slot]);
-          if (s == stages - 1) mma_commit(&t_full[buf]);
+          for (int k = 1; k < KS / 16; ++k)
+            mma_f16<PAIR>(d, dw + (GRAD ? 128 : 2) * k, dx + 2 * k, idesc, 1);
+          commit<PAIR>(&empty[slot]);
+          more = 1;
+          dx += X_BYTES >> 4;
+          dw += W_BYTES >> 4;
+          if (++slot == STAGES) {
+            slot = 0;
+            par ^= 1;
+            dx = dx0;
+            dw = dw0;
+          }
         }
-        __syncwarp();
+        if (ok) commit<PAIR>(&t_full[buf]);
       }
-    }
-    if (!ok) {  // MMAs in flight end before their operands or TMEM go away
-      if (lane == 0) mma_commit(drain);
-      __syncwarp();
-      warp_wait(drain, 0, status);
+      if (!ok) {  // MMAs in flight end before their operands or TMEM go away
+        commit<PAIR>(drain);
+        mbar_poll(drain, 0, status);
+      }
     }
   } else if (warp >= CONV_WARP0) {
     // ---------------- expansion ----------------
-    const int tid = threadIdx.x - CONV_WARP0 * 32;
+    const uint32_t group = (uint32_t)(warp - CONV_WARP0) / CONV_WARPS;
+    const int tid = (threadIdx.x - CONV_WARP0 * 32) % (CONV_WARPS * 32);
     // forward: row n (of 128), half of its 64 k; gradient: row n (of 64),
     // quarter of its 128 k.  32 weights, one group, 16 nibble bytes each.
     const int row = GRAD ? tid >> 2 : tid >> 1, part = GRAD ? tid & 3 : tid & 1;
     const uint32_t nib_at = (uint32_t)(tid * 16);
     const int G = c.K >> 5;
-    uint32_t it = 0;
+    constexpr int SB = FMT == QG_W4_BF16 ? 2 : 4;
+    const int64_t zoff = (int64_t)c.N * G * 4;
+    // gradient: parts 2 and 3 go 8 KiB behind 0 and 1, to the same banks, so
+    // they store their words in the order 2, 3, 0, 1
+    const bool turn = GRAD && part >= 2;
+    const int c0 = GRAD ? (part & 1) * 4 + (turn ? 2 : 0) : part * 4;
+    const uint32_t w_at = sW + (GRAD ? (part >> 1) * 8192 + row * 128 : row * 128);
+    const uint32_t step_b = GRAD ? (uint32_t)(KS * G * SB) : 2u * SB;  // scales: stage to stage
+    uint32_t it = 0, slot = group, ns = group;
+    uint32_t par = 1, npar = 0;  // parities of the waits for a free slot and for nibbles
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
       const uint8_t* scl = c.packed + (int64_t)tl.e * c.expert_bytes + (int64_t)c.N * (c.K >> 1);
-      const uint8_t* zer = scl + (int64_t)c.N * G * 4;
+      const int g = GRAD ? (tl.f0 >> 5) + part : part;
+      const int n0 = GRAD ? row : tl.f0 + row;
+      scl += ((int64_t)n0 * G + g) * SB;
+      // rows of W from this one on (gradient: 64 further with every stage)
+      const int left = GRAD && g >= G ? 0 : c.N - n0;
       auto fetch = [&](int s) {
-        const int n = GRAD ? s * KS + row : tl.f0 + row;
-        const int g = GRAD ? (tl.f0 >> 5) + part : 2 * s + part;
-        return load_scale<FMT>(scl, zer, (int64_t)n * G + g, s < stages && n < c.N && g < G);
+        return load_scale<FMT>(scl + (int64_t)s * step_b, zoff, s < stages && (GRAD ? KS * s : 0) < left);
       };
-      uint2 s0 = fetch(0), s1 = fetch(1);
-      for (int s = 0; s < stages; ++s, ++it) {
-        const int slot = it % STAGES, ns = it % NRING;
-        const uint2 s2 = fetch(s + 2);  // two stages ahead
-        ok = warp_wait(&n_full[ns], (it / NRING) & 1, status);
+      int s = (it & 1) == group ? 0 : 1;  // this group's stages: every other one
+      uint2 now = fetch(s), next = fetch(s + 2);
+      for (; s < stages; s += 2) {
+        ok = warp_wait(&n_full[ns], npar, status);
         if (!ok) break;
         uint4 q;
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
                      : "r"(sN + ns * NIB_BYTES + nib_at)
                      : "memory");
-        const Scale<FMT> sc = make_scale<FMT>(s0);
-        if (it >= STAGES) ok = warp_wait(&empty[slot], ((it / STAGES) - 1) & 1, status);
-        if (!ok) break;
-        // gradient: parts 2 and 3 go 8 KiB behind 0 and 1, to the same banks,
-        // so they store their words in the order 2, 3, 0, 1
-        const bool turn = GRAD && part >= 2;
+        const Scale<FMT> sc = make_scale<FMT>(now);
+        now = next;
+        next = fetch(s + 4);
         const uint32_t wd[4] = {turn ? q.z : q.x, turn ? q.w : q.y, turn ? q.x : q.z, turn ? q.y : q.w};
-        const uint32_t dst = GRAD ? sW + slot * W_BYTES + (part >> 1) * 8192 + row * 128
-                                  : sW + slot * W_BYTES + row * 128;
-        const int c0 = GRAD ? (part & 1) * 4 + (turn ? 2 : 0) : part * 4;
+        uint32_t o[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[4];
-          expand8<FMT>(wd[i], sc, o);
+        for (int i = 0; i < 4; ++i) expand8<FMT>(wd[i], sc, o[i]);
+        ok = warp_wait(&empty[slot], par, status);  // the first round passes
+        if (!ok) break;
+        const uint32_t dst = w_at + slot * W_BYTES;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (((c0 ^ i) ^ (row & 7)) << 4)),
-                       "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                       "r"(o[i][0]), "r"(o[i][1]), "r"(o[i][2]), "r"(o[i][3])
                        : "memory");
-        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&n_empty[ns]);
-          mbar_arrive(&w_full[slot]);
+          if constexpr (PAIR) mbar_arrive_cluster(mapa(smem_u32(&full[slot]), 0));
+          else mbar_arrive(&full[slot]);
         }
-        s0 = s1;
-        s1 = s2;
+        if ((slot += 2) >= STAGES) {
+          slot -= STAGES;
+          par ^= 1;
+        }
+        if ((ns += 2) >= NRING) {
+          ns -= NRING;
+          npar ^= 1;
+        }
       }
+      it += (uint32_t)stages;
     }
   } else if (warp >= EPI_WARP0) {
     // ---------------- epilogue ----------------
@@ -473,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool even = (lane & 1) == 0;
     const bool vec = ((reinterpret_cast<uintptr_t>(c.out) & 3) == 0) && ((c.ld_out & 1) == 0);
     uint32_t use = 0;
-    for (int64_t t = blockIdx.x; t < total; t += gridDim.x, ++use) {
+    for (int64_t t = first; t < total; t += step, ++use) {
       const Tile tl = tile_at(t);
       const uint32_t buf = use & 1;
       if (!warp_wait(&t_full[buf], (use >> 1) & 1, status)) break;
@@ -513,18 +585,57 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&t_empty[buf]);
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(mapa(smem_u32(&t_empty[buf]), 0));
+        else mbar_arrive(&t_empty[buf]);
+      }
     }
   }
 
+  // no CTA of a pair leaves while the other may still signal its barriers or
+  // read its shared memory
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all(); else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512)
-                 : "memory");
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512)
+                   : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512)
+                   : "memory");
   }
+}
+
+// Rows into sorted order: xs[p] = x[src[p] / topk] for the rows that belong
+// to an expert, a warp per row.
+__global__ void __launch_bounds__(256) a16w4_gather_kernel(const __grid_constant__ A16W4Call c,
+                                                           uint16_t* __restrict__ xs, int* status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int p = (int)(blockIdx.x * 8 + (threadIdx.x >> 5));
+  if (p < c.offsets[0] || p >= min(c.offsets[c.E], c.S)) return;
+  const int s = c.src[p];
+  const int row = s < 0 ? c.in_rows : s / c.topk;
+  const int nv = c.K / 8;  // K % 64 == 0 and 16-byte aligned rows
+  uint4* dst = reinterpret_cast<uint4*>(xs + (int64_t)p * c.K);
+  if (row >= c.in_rows) {  // outside x: zeros
+    record_error(status, QG_ERR_INVALID_ARG);
+    for (int i = lane; i < nv; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const uint4* from = reinterpret_cast<const uint4*>(c.in + row * c.ld_in);
+  int i = lane;
+  for (; i + 96 < nv; i += 128) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __ldg(from + i + 32 * k);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dst[i + 32 * k] = v[k];
+  }
+  for (; i < nv; i += 32) dst[i] = __ldg(from + i);
 }
 
 // ---------------------------------------------------------------------------
@@ -533,16 +644,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 PFN_cuTensorMapEncodeTiled_v12000 g_tc_encode = nullptr;
 
 template <int FMT>
-const void* kernel_of(bool grad, bool gather) {
-  if (grad) return (const void*)a16w4_tc_kernel<FMT, true, false>;
-  return gather ? (const void*)a16w4_tc_kernel<FMT, false, true>
-                : (const void*)a16w4_tc_kernel<FMT, false, false>;
+const void* kernel_of(bool grad, bool pair) {
+  if (grad) return pair ? (const void*)a16w4_tc_kernel<FMT, true, true> : (const void*)a16w4_tc_kernel<FMT, true, false>;
+  return pair ? (const void*)a16w4_tc_kernel<FMT, false, true> : (const void*)a16w4_tc_kernel<FMT, false, false>;
 }
-const void* kernel_of(int fmt, bool grad, bool gather) {
-  if (fmt == QG_W4_F32) return kernel_of<QG_W4_F32>(grad, gather);
-  if (fmt == QG_W4_BF16) return kernel_of<QG_W4_BF16>(grad, gather);
-  return kernel_of<QG_W4_ASYM>(grad, gather);
+const void* kernel_of(int fmt, bool grad, bool pair) {
+  if (fmt == QG_W4_F32) return kernel_of<QG_W4_F32>(grad, pair);
+  if (fmt == QG_W4_BF16) return kernel_of<QG_W4_BF16>(grad, pair);
+  return kernel_of<QG_W4_ASYM>(grad, pair);
 }
+
+constexpr int kMaxDevices = 64;
+int g_tc_pairs[kMaxDevices];  // CTA pairs that can be resident at once (0: not asked yet)
 
 }  // namespace
 
@@ -555,22 +668,73 @@ int a16w4_tc_setup() {
     return QG_ERR_CUDA;
   g_tc_encode = (PFN_cuTensorMapEncodeTiled_v12000)fn;
   for (int fmt = 0; fmt < 3; ++fmt)
-    for (int v = 0; v < 3; ++v)
-      if (cudaFuncSetAttribute(kernel_of(fmt, v == 2, v == 1),
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)tc_smem(kA16W4MaxExperts)) != cudaSuccess)
+    for (int v = 0; v < 4; ++v) {
+      const bool pair = v & 1;
+      const size_t most = pair ? tc_smem<true>(kA16W4MaxExperts) : tc_smem<false>(kA16W4MaxExperts);
+      if (cudaFuncSetAttribute(kernel_of(fmt, v >= 2, pair), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)most) != cudaSuccess)
         return QG_ERR_CUDA;
+    }
+  // how many pairs can be resident at once (an SM whose partner is disabled
+  // cannot host one)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QG_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = tc_smem<true>(kA16W4MaxExperts);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int pairs = 0;
+  if (cudaOccupancyMaxActiveClusters(&pairs, kernel_of(QG_W4_F32, false, true), &cfg) != cudaSuccess ||
+      pairs < 1)
+    return QG_ERR_CUDA;
+  g_tc_pairs[dev] = pairs;
   return QG_OK;
 }
 
-int launch_a16w4_tc(const A16W4Call& c, bool grad, cudaStream_t st) {
+size_t a16w4_tc_workspace(int S, int K, bool gather) {
+  return gather ? (size_t)S * K * 2 : 0;
+}
+
+int launch_a16w4_tc(const A16W4Call& call, bool grad, void* ws, cudaStream_t st) {
+  A16W4Call c = call;
+  int* status = status_word();
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (c.src) {
+    cfg.gridDim = dim3((unsigned)cdiv(c.S, 8));
+    cfg.blockDim = dim3(256);
+    if (cudaLaunchKernelEx(&cfg, a16w4_gather_kernel, c, (uint16_t*)ws, status) != cudaSuccess)
+      return QG_ERR_CUDA;
+    c.in = (const uint16_t*)ws;
+    c.ld_in = c.K;
+    c.in_rows = c.S;
+    c.src = nullptr;
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QG_ERR_CUDA;
   TcArgs a{};
   a.c = c;
   a.F = grad ? c.K : c.N;
   a.R = grad ? c.N : c.K;
-  a.ftiles = (int)cdiv(a.F, TF);
   a.stages = (int)cdiv(a.R, KS);
-  const bool gather = c.src != nullptr;
+  // at most this many tiles of rows: every expert's last one may be partial
+  const int64_t row_tiles = c.offsets ? cdiv(c.S, TT) + min64(c.E, c.S) : cdiv(c.S, TT);
+  // pairs, unless their tiles leave half of the SMs without work
+  const int64_t likely = c.offsets ? max64(cdiv(c.S, TT), min64(c.E, c.S)) : row_tiles;
+  const bool pair = likely * cdiv(a.F, 2 * TF) * 4 > num_sms();
+  a.ftiles = (int)cdiv(a.F, pair ? 2 * TF : TF);
   TcMaps m;
   {
     cuuint64_t dims[3] = {(cuuint64_t)c.K / 8, (cuuint64_t)c.N, (cuuint64_t)c.E};
@@ -588,7 +752,7 @@ int launch_a16w4_tc(const A16W4Call& c, bool grad, cudaStream_t st) {
   {
     cuuint64_t dims[2] = {(cuuint64_t)a.R, (cuuint64_t)c.in_rows};
     cuuint64_t strides[1] = {(cuuint64_t)c.ld_in * 2};
-    cuuint32_t box[2] = {KS, gather ? 1u : (cuuint32_t)XBOX};
+    cuuint32_t box[2] = {KS, XBOX};
     cuuint32_t es[2] = {1, 1};
     if (g_tc_encode(&m.rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (void*)c.in, dims, strides, box, es,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -596,23 +760,20 @@ int launch_a16w4_tc(const A16W4Call& c, bool grad, cudaStream_t st) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return QG_ERR_CUDA;
   }
-  // at most this many tiles: every expert's last tile may be a partial one
-  const int64_t most = (cdiv(c.S, TT) + min64(c.E, c.S)) * a.ftiles;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)min64(num_sms(), c.offsets ? most : cdiv(c.S, TT) * a.ftiles));
+  const int64_t most = row_tiles * a.ftiles;
+  cfg.gridDim = dim3(pair ? 2 * (unsigned)min64(g_tc_pairs[dev], most) : (unsigned)min64(num_sms(), most));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = tc_smem(c.E);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int* status = status_word();
+  cfg.dynamicSmemBytes = pair ? tc_smem<true>(c.E) : tc_smem<false>(c.E);
+  if (pair) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
   void* args[] = {&m, &a, &status};
-  return cudaLaunchKernelExC(&cfg, kernel_of(c.format, grad, gather), args) == cudaSuccess
-             ? QG_OK
-             : QG_ERR_CUDA;
+  return cudaLaunchKernelExC(&cfg, kernel_of(c.format, grad, pair), args) == cudaSuccess ? QG_OK
+                                                                                        : QG_ERR_CUDA;
 }
 
 }  // namespace qg

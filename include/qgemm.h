@@ -448,14 +448,18 @@ int qgemm_a16w4_bf16(int M, int N, int K, const void* x, int64_t ldx, const void
  *   y: bf16 [S][ldy].  Rows that belong to no expert (before offsets[0],
  *   from offsets[E] on) are left as they are.
  * E <= 1024, K % 64 == 0 (else QG_ERR_UNSUPPORTED).  Nothing is read back to
- * the host.  An expert whose range is not inside [0, S) gets no rows, and a
+ * the host.  Workspace: qgemm_a16w4_bf16_experts_workspace_bytes(E, S, K,
+ * src != NULL), 256-byte aligned (0: none; with src and many rows per expert
+ * the rows are first brought into sorted order there).  An expert whose range is not inside [0, S) gets no rows, and a
  * src entry that reaches outside x counts as a row of zeros; both record
  * QG_ERR_INVALID_ARG in the device status.
  */
+size_t qgemm_a16w4_bf16_experts_workspace_bytes(int E, int S, int K, int indirect);
 int qgemm_a16w4_bf16_experts(int E, int S, int N, int K, const void* x, int64_t ldx, int x_rows,
                              const int32_t* src, int topk, const int32_t* offsets,
                              const void* packed_w, int64_t expert_bytes, int format,
-                             const float* bias, void* y, int64_t ldy, void* stream);
+                             const float* bias, void* y, int64_t ldy, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /*
  * Gradients of the two products with respect to their rows, for training
