@@ -154,6 +154,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Every lane waits; the warp takes its decision together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status) {
   // a phase that is complete is seen at once; a parked wait costs about 180
@@ -421,11 +429,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     // One thread, and every stage passes through it: with divisions by the
     // ring's size, two barriers a stage and polled waits it took 1050 cycles a
     // stage, twice the MMAs' own time.
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       uint32_t use = 0, slot = 0, par = 0;
       bool ok = true;
-      const uint64_t dx0 = sdesc_sw128(sX), dw0 = GRAD ? sdesc_mn_sw128(sW) : sdesc_sw128(sW);
-      uint64_t dx = dx0, dw = dw0;  // of the slot; descriptor addresses count 16 bytes
       for (int64_t t = first; t < total && ok; t += step, ++use) {
         const Tile tl = tile_at(t);
         const int n = (tl.np + kRowStep - 1) & ~(kRowStep - 1);
@@ -433,35 +439,34 @@ __global__ void __launch_bounds__(THREADS, 1)
                                ((uint32_t)(n >> 3) << 17) |
                                ((uint32_t)((PAIR ? 2 * TF : TF) >> 4) << 24);
         const uint32_t buf = use & 1;
-        ok = mbar_wait(&t_empty[buf], ((use >> 1) & 1) ^ 1, status);
+        ok = warp_wait(&t_empty[buf], ((use >> 1) & 1) ^ 1, status);
         const uint32_t d = tmem_base + buf * TT;
-        uint32_t more = 0;  // the tile's first MMA overwrites
         for (int s = 0; s < stages && ok; ++s) {
-          ok = mbar_wait(&full[slot], par, status);
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], par, status));
           if (!ok) break;
           tc_fence_after();
-          // 16 k further is 32 bytes of a K-major row, or 16 rows of 128
-          // bytes of the MN-major tile
-          mma_f16<PAIR>(d, dw, dx, idesc, more);
+          if (elect_one()) {
+            // descriptor addresses count 16 bytes: 16 k further is 32 bytes
+            // of a K-major row, or 16 rows of 128 bytes of the MN-major tile
+            const uint64_t dx = sdesc_sw128(sX + slot * X_BYTES);
+            const uint64_t dw = GRAD ? sdesc_mn_sw128(sW + slot * W_BYTES) : sdesc_sw128(sW + slot * W_BYTES);
 #pragma unroll
-          for (int k = 1; k < KS / 16; ++k)
-            mma_f16<PAIR>(d, dw + (GRAD ? 128 : 2) * k, dx + 2 * k, idesc, 1);
-          commit<PAIR>(&empty[slot]);
-          more = 1;
-          dx += X_BYTES >> 4;
-          dw += W_BYTES >> 4;
+            for (int k = 0; k < KS / 16; ++k)
+              mma_f16<PAIR>(d, dw + (GRAD ? 128 : 2) * k, dx + 2 * k, idesc, s > 0 || k > 0);
+            commit<PAIR>(&empty[slot]);
+            if (s == stages - 1) commit<PAIR>(&t_full[buf]);
+          }
+          __syncwarp();
           if (++slot == STAGES) {
             slot = 0;
             par ^= 1;
-            dx = dx0;
-            dw = dw0;
           }
         }
-        if (ok) commit<PAIR>(&t_full[buf]);
       }
       if (!ok) {  // MMAs in flight end before their operands or TMEM go away
-        commit<PAIR>(drain);
-        mbar_poll(drain, 0, status);
+        if (elect_one()) commit<PAIR>(drain);
+        __syncwarp();
+        warp_wait(drain, 0, status);
       }
     }
   } else if (warp >= CONV_WARP0) {
