@@ -199,23 +199,73 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 // ---------------------------------------------------------------------------
 // Rows
 // ---------------------------------------------------------------------------
-// V values of type T as one access of V * sizeof(T) bytes.
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-  T v[V];
+// V values of type T as one access of V * sizeof(T) bytes, kept as raw words
+// until they are used (as arrays of 16-bit values the compiler widens them on
+// arrival and runs out of registers).
+template <typename T, int V, typename W = uint32_t, int N = (int)(sizeof(T) * V / sizeof(W))>
+struct alignas(sizeof(T) * V) Words {
+  W w[N];
 };
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T, int V>
+struct Pack : Words<T, V> {};
 template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
-  return __float2bfloat16_rn(v);
+struct Pack<T, 1> : Words<T, 1, T, 1> {};  // a value on its own
+
+__device__ __forceinline__ void unpack(const Words<float, 4>& p, float (&f)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(p.w[k]);
+}
+template <int V>
+__device__ __forceinline__ void unpack(const Words<__nv_bfloat16, V>& p, float (&f)[V]) {
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) {
+    f[2 * k] = __uint_as_float(p.w[k] << 16);
+    f[2 * k + 1] = __uint_as_float(p.w[k] & 0xFFFF0000u);
+  }
+}
+template <int V>
+__device__ __forceinline__ void unpack(const Words<__half, V>& p, float (&f)[V]) {
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p.w[k]));
+    f[2 * k] = v.x;
+    f[2 * k + 1] = v.y;
+  }
+}
+__device__ __forceinline__ void unpack(const Pack<float, 1>& p, float (&f)[1]) { f[0] = p.w[0]; }
+__device__ __forceinline__ void unpack(const Pack<__half, 1>& p, float (&f)[1]) {
+  f[0] = __half2float(p.w[0]);
+}
+__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, 1>& p, float (&f)[1]) {
+  f[0] = __bfloat162float(p.w[0]);
+}
+
+__device__ __forceinline__ void pack(const float (&f)[4], Words<float, 4>& p) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) p.w[k] = __float_as_uint(f[k]);
+}
+template <int V>
+__device__ __forceinline__ void pack(const float (&f)[V], Words<__nv_bfloat16, V>& p) {
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+    p.w[k] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+template <int V>
+__device__ __forceinline__ void pack(const float (&f)[V], Words<__half, V>& p) {
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) {
+    const __half2 v = __floats2half2_rn(f[2 * k], f[2 * k + 1]);
+    p.w[k] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+__device__ __forceinline__ void pack(const float (&f)[1], Pack<float, 1>& p) { p.w[0] = f[0]; }
+__device__ __forceinline__ void pack(const float (&f)[1], Pack<__half, 1>& p) {
+  p.w[0] = __float2half_rn(f[0]);
+}
+__device__ __forceinline__ void pack(const float (&f)[1], Pack<__nv_bfloat16, 1>& p) {
+  p.w[0] = __float2bfloat16_rn(f[0]);
 }
 
 // Sorted position of (t, j), or -1 when the entry has no expert.  A position
@@ -267,7 +317,7 @@ __global__ void __launch_bounds__(256)
 // a row's load between two checks of positions waited for the one before it
 // (8192 tokens x 8 rows of 4096 bf16: 282 us).
 template <typename T, int V>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
     combine_rows_kernel(int topk, int64_t S, int64_t nv, const T* __restrict__ ys, int64_t ldys,
                         const int32_t* __restrict__ pos, const float* __restrict__ w,
                         T* __restrict__ y, int64_t ldy, int* status) {
@@ -295,17 +345,18 @@ __global__ void __launch_bounds__(256)
       P r[JB];
 #pragma unroll
       for (int j = 0; j < JB; ++j)
-        if (p[j] >= 0) r[j] = reinterpret_cast<const P*>(ys + p[j] * ldys)[i];
+        if (p[j] >= 0) r[j] = reinterpret_cast<const P*>(ys + (int64_t)p[j] * ldys)[i];
 #pragma unroll
       for (int j = 0; j < JB; ++j) {
         if (p[j] < 0) continue;
+        float v[V];
+        unpack(r[j], v);
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = fmaf(wj[j], to_f32(r[j].v[k]), acc[k]);
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(wj[j], v[k], acc[k]);
       }
     }
     P out;
-#pragma unroll
-    for (int k = 0; k < V; ++k) out.v[k] = from_f32<T>(acc[k]);
+    pack(acc, out);
     reinterpret_cast<P*>(y + t * ldy)[i] = out;
   }
 }
@@ -326,7 +377,7 @@ __global__ void __launch_bounds__(512)
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   for (int jb = 0; jb < topk; jb += JB) {
-    int64_t p[JB];
+    int p[JB];
     float wj[JB], dot[JB];
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
@@ -336,24 +387,29 @@ __global__ void __launch_bounds__(512)
     }
     for (int64_t i = threadIdx.x; i < nv; i += blockDim.x) {
       const P g = reinterpret_cast<const P*>(dy + t * lddy)[i];
+      float gf[V];
+      unpack(g, gf);
       P r[JB];
       if (dw) {
 #pragma unroll
         for (int j = 0; j < JB; ++j)
-          if (p[j] >= 0) r[j] = reinterpret_cast<const P*>(ys + p[j] * ldys)[i];
+          if (p[j] >= 0) r[j] = reinterpret_cast<const P*>(ys + (int64_t)p[j] * ldys)[i];
       }
 #pragma unroll
       for (int j = 0; j < JB; ++j) {
         if (p[j] < 0) continue;
+        float v[V];
         if (dw) {
+          unpack(r[j], v);
 #pragma unroll
-          for (int k = 0; k < V; ++k) dot[j] = fmaf(to_f32(g.v[k]), to_f32(r[j].v[k]), dot[j]);
+          for (int k = 0; k < V; ++k) dot[j] = fmaf(gf[k], v[k], dot[j]);
         }
         if (dys) {
           P out;
 #pragma unroll
-          for (int k = 0; k < V; ++k) out.v[k] = from_f32<T>(wj[j] * to_f32(g.v[k]));
-          reinterpret_cast<P*>(dys + p[j] * lddys)[i] = out;
+          for (int k = 0; k < V; ++k) v[k] = wj[j] * gf[k];
+          pack(v, out);
+          reinterpret_cast<P*>(dys + (int64_t)p[j] * lddys)[i] = out;
         }
       }
     }
