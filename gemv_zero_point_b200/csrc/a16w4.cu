@@ -138,6 +138,7 @@ struct RowsArgs {
   A16W4Call c;
   int chunks;        // ceil(K / KC)
   int wk;            // warps that split K; W / wk warps split the rows
+  int per_sm;        // CTAs an SM
   int share, more;   // dense: 8-row blocks of a CTA, and how many CTAs take one more
 };
 
@@ -167,8 +168,9 @@ struct Shares {
         rw((int)(threadIdx.x >> 5) / a_.wk) {
     const A16W4Call& c = a.c;
     if (DENSE) {
-      v0 = 8 * ((int64_t)a.share * blockIdx.x + min(a.more, (int)blockIdx.x));
-      v1 = min64(v0 + 8 * (a.share + ((int)blockIdx.x < a.more ? 1 : 0)), c.N);
+      const int b = (int)blockIdx.x;
+      v0 = 8 * ((int64_t)a.share * b + min(a.more, b));
+      v1 = min64(v0 + 8 * (a.share + (b < a.more ? 1 : 0)), c.N);
       return;
     }
     const int lane = threadIdx.x & 31;
@@ -275,7 +277,8 @@ struct Shares {
     }
     return row;
   }
-  // one whole run into L2, and on to the next
+  // One whole run into L2, and on to the next (few and large requests: each
+  // costs the copy engine some 100 ns).
   __device__ __forceinline__ void prefetch(Run& r, int sb, int64_t zoff, bool zeros) const {
     if (r.left <= 0) return;
     const int rowb = a.c.K >> 1, G = a.c.K >> 5;
@@ -319,7 +322,7 @@ __device__ __forceinline__ void sum_and_store(const A16W4Call& c, const Run& at,
 // ---------------------------------------------------------------------------
 // NT: MMA column blocks (8 tokens) per pass.
 template <int FMT, int NT, bool DENSE>
-__global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(W * 32, NT == 1 ? 2 : 1)
     a16w4_rows_kernel(const __grid_constant__ RowsArgs a, int* status) {
   using Sl = Slot<FMT>;
   extern __shared__ __align__(128) uint8_t sm[];
@@ -424,6 +427,37 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1)
   const uint32_t a_at = ring + (uint32_t)(((lane & 15) * 64) + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4));
   const uint32_t s_at = ring + Sl::OFF_SCL + (uint32_t)(g * Sl::SCL);
 
+  // this lane's token rows (MMA column g); columns past the last token repeat
+  // it, and are not stored
+  const uint16_t* xr[NT];
+  auto point_x = [&](const Run& r) {
+    const int p0 = sh.tokens_from(r), np = sh.tokens(r);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = sh.input_row(p0 + min(8 * n + g, np - 1), status);
+      xr[n] = row < 0 ? nullptr : c.in + row * c.ld_in + t * 8;
+    }
+  };
+  // B fragments: lane t gives x[8t .. 8t+7] of its group, as A's words do.
+  // Up to 16 tokens the next chunk is read ahead; more have no registers left
+  // for that.
+  constexpr bool AHEAD = NT <= 2;
+  uint4 xb[NT][4], xn[NT][4];
+  auto load_x = [&](uint4 (&x)[NT][4], int ch) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        x[n][q] = make_uint4(0, 0, 0, 0);
+        if (xr[n] && 4 * ch + q < G)
+          x[n][q] = *reinterpret_cast<const uint4*>(xr[n] + (int64_t)ch * KC + q * 32);
+      }
+  };
+  if (at.nrows > 0) {
+    point_x(at);
+    if (AHEAD) load_x(xn, ch0);
+  }
+
   // every warp walks every run: its chunks, then the sum over the K warps
   int slot = 0;
   while (at.left > 0) {
@@ -436,36 +470,15 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[i][n][k] = 0.0f;
     if (at.nrows > 0) {
-      // this lane's token rows (MMA column g); columns past the last token
-      // repeat it, and are not stored
-      const uint16_t* xr[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int row = sh.input_row(p0 + min(8 * n + g, np - 1), status);
-        xr[n] = row < 0 ? nullptr : c.in + row * c.ld_in + t * 8;
-      }
-      // B fragments: lane t gives x[8t .. 8t+7] of its group, as A's words do
-      uint4 xb[NT][4], xn[NT][4];
-      auto load_x = [&](uint4 (&x)[NT][4], int ch) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            x[n][q] = make_uint4(0, 0, 0, 0);
-            if (xr[n] && 4 * ch + q < G)
-              x[n][q] = *reinterpret_cast<const uint4*>(xr[n] + (int64_t)ch * KC + q * 32);
-          }
-      };
-      // one block of tokens: the next chunk is read ahead; more of them have
-      // no registers left for that
-      load_x(NT == 1 ? xn : xb, ch0);
       for (int ch = ch0; ch < ch1; ++ch) {
         const bool half = 4 * ch + 4 > G;  // x is 0 for groups 2 and 3
-        if (NT == 1) {
+        if (AHEAD) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) xb[0][q] = xn[0][q];
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) xb[n][q] = xn[n][q];
           if (ch + 1 < ch1) load_x(xn, ch + 1);
-        } else if (ch > ch0) {
+        } else {
           load_x(xb, ch);
         }
         // -136 X of this lane's tokens 2t, 2t + 1
@@ -564,11 +577,18 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1)
         }
       }
     }
+    // the next run's first x, before the sums of this one
+    Run nx = at;
+    sh.next(nx);
+    if (nx.nrows > 0) {
+      if (!DENSE && (nx.e != at.e || nx.pass != at.pass)) point_x(nx);
+      if (AHEAD) load_x(xn, ch0);
+    }
     if (threadIdx.x == 0) sh.prefetch(ahead, SB, zoff, FMT == QG_W4_ASYM);
     __syncthreads();
     sum_and_store(c, at, p0, np, 8 * NT, wk, part, prows);
     __syncthreads();
-    sh.next(at);
+    at = nx;
   }
   cp_wait<0>();
 }
@@ -583,7 +603,7 @@ size_t rows_smem(int fmt, int nt, int wk, int E) {
 template <int FMT, int NT, bool DENSE>
 int run_rows(RowsArgs a, cudaStream_t st) {
   const size_t smem = rows_smem(FMT, NT, a.wk, a.c.E);
-  int ctas = num_sms() * (NT <= 2 && smem <= 113 * 1024 ? 2 : 1);
+  int ctas = num_sms() * (a.per_sm == 2 && NT == 1 && smem <= 113 * 1024 ? 2 : 1);
   if (DENSE) {  // in blocks of 8 rows, half an MMA tile
     const int blocks = (int)cdiv(a.c.N, 8);
     ctas = (int)min64(ctas, blocks);
@@ -656,11 +676,19 @@ int launch_a16w4_rows(const A16W4Call& c, cudaStream_t st) {
   RowsArgs a{};
   a.c = c;
   a.chunks = (int)cdiv(c.K, KC);
-  a.wk = 1;
-  while (a.wk * 2 <= W && a.wk * 2 <= a.chunks) a.wk *= 2;
   // tokens per pass: what one expert has, as far as the host knows
   const int64_t each = cdiv(c.S, c.E);
   const int nt = each <= 8 ? 1 : each <= 16 ? 2 : 4;
+  // weight rows of an SM, as far as the host knows
+  const int64_t share = min64(c.E, c.S) * c.N / num_sms();
+  // Two CTAs an SM hide each other's start and sums, but each reads all of x:
+  // one where an SM has no more than a run's rows.
+  a.per_sm = share > WROWS ? 2 : 1;
+  // All warps split K, except where a CTA has rows for two row warps and K
+  // would leave each warp less than four chunks between two sums.
+  a.wk = 1;
+  while (a.wk * 2 <= W && a.wk * 2 <= a.chunks) a.wk *= 2;
+  while (a.wk > 1 && a.chunks < 4 * a.wk && share >= 4 * WROWS * (W / a.wk)) a.wk /= 2;
   if (c.format == QG_W4_F32) return run_rows_nt<QG_W4_F32>(nt, a, st);
   if (c.format == QG_W4_BF16) return run_rows_nt<QG_W4_BF16>(nt, a, st);
   return run_rows_nt<QG_W4_ASYM>(nt, a, st);
