@@ -439,10 +439,7 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 2 : 1)
     }
   };
   // B fragments: lane t gives x[8t .. 8t+7] of its group, as A's words do.
-  // Up to 16 tokens the next chunk is read ahead; more have no registers left
-  // for that.
-  constexpr bool AHEAD = NT <= 2;
-  uint4 xb[NT][4], xn[NT][4];
+  uint4 xb[NT][4], xn[NT][4];  // this chunk, and the next one read ahead
   auto load_x = [&](uint4 (&x)[NT][4], int ch) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -455,7 +452,7 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 2 : 1)
   };
   if (at.nrows > 0) {
     point_x(at);
-    if (AHEAD) load_x(xn, ch0);
+    load_x(xn, ch0);
   }
 
   // every warp walks every run: its chunks, then the sum over the K warps
@@ -472,15 +469,11 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 2 : 1)
     if (at.nrows > 0) {
       for (int ch = ch0; ch < ch1; ++ch) {
         const bool half = 4 * ch + 4 > G;  // x is 0 for groups 2 and 3
-        if (AHEAD) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) xb[n][q] = xn[n][q];
-          if (ch + 1 < ch1) load_x(xn, ch + 1);
-        } else {
-          load_x(xb, ch);
-        }
+          for (int q = 0; q < 4; ++q) xb[n][q] = xn[n][q];
+        if (ch + 1 < ch1) load_x(xn, ch + 1);
         // -136 X of this lane's tokens 2t, 2t + 1
         float z[NT][4][2];
 #pragma unroll
@@ -582,7 +575,7 @@ __global__ void __launch_bounds__(W * 32, NT == 1 ? 2 : 1)
     sh.next(nx);
     if (nx.nrows > 0) {
       if (!DENSE && (nx.e != at.e || nx.pass != at.pass)) point_x(nx);
-      if (AHEAD) load_x(xn, ch0);
+      load_x(xn, ch0);
     }
     if (threadIdx.x == 0) sh.prefetch(ahead, SB, zoff, FMT == QG_W4_ASYM);
     __syncthreads();
@@ -627,14 +620,8 @@ int run_rows(RowsArgs a, cudaStream_t st) {
 
 template <int FMT>
 int run_rows_nt(int nt, const RowsArgs& a, cudaStream_t st) {
-  if (!a.c.offsets) {
-    if (nt == 1) return run_rows<FMT, 1, true>(a, st);
-    if (nt == 2) return run_rows<FMT, 2, true>(a, st);
-    return run_rows<FMT, 4, true>(a, st);
-  }
-  if (nt == 1) return run_rows<FMT, 1, false>(a, st);
-  if (nt == 2) return run_rows<FMT, 2, false>(a, st);
-  return run_rows<FMT, 4, false>(a, st);
+  if (!a.c.offsets) return nt == 1 ? run_rows<FMT, 1, true>(a, st) : run_rows<FMT, 2, true>(a, st);
+  return nt == 1 ? run_rows<FMT, 1, false>(a, st) : run_rows<FMT, 2, false>(a, st);
 }
 
 template <int FMT, int NT, bool DENSE>
@@ -655,10 +642,8 @@ template <int FMT>
 int set_rows_smem_nt() {
   int rc = set_rows_smem<FMT, 1, true>();
   if (rc == QG_OK) rc = set_rows_smem<FMT, 2, true>();
-  if (rc == QG_OK) rc = set_rows_smem<FMT, 4, true>();
   if (rc == QG_OK) rc = set_rows_smem<FMT, 1, false>();
   if (rc == QG_OK) rc = set_rows_smem<FMT, 2, false>();
-  if (rc == QG_OK) rc = set_rows_smem<FMT, 4, false>();
   return rc;
 }
 
@@ -678,7 +663,7 @@ int launch_a16w4_rows(const A16W4Call& c, cudaStream_t st) {
   a.chunks = (int)cdiv(c.K, KC);
   // tokens per pass: what one expert has, as far as the host knows
   const int64_t each = cdiv(c.S, c.E);
-  const int nt = each <= 8 ? 1 : each <= 16 ? 2 : 4;
+  const int nt = each <= 8 ? 1 : 2;
   // weight rows of an SM, as far as the host knows
   const int64_t share = min64(c.E, c.S) * c.N / num_sms();
   // Two CTAs an SM hide each other's start and sums, but each reads all of x:
@@ -709,8 +694,9 @@ int64_t packed_bytes(int N, int K, int format) {
 }
 
 // Few rows per expert stream the weights past warp MMAs, more go to the
-// tensor cores.
-bool few_rows(int E, int S) { return cdiv(S, E) <= 32; }
+// tensor cores: 16 rows at N = 14336, K = 4096 take 19 us here and 26 there,
+// 32 rows 34 (in blocks of 32) and 26.
+bool few_rows(int E, int S) { return cdiv(S, E) <= 16; }
 
 // Checks of every product: QG_OK when the call can run (S may be 0).
 int product_args(int E, int S, int N, int K, const void* in, int64_t ld_in, int in_cols,
