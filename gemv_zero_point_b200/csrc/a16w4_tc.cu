@@ -12,17 +12,23 @@
 // price of one MMA per weight; the sums stay in f32 (TMEM) and the output is
 // rounded once.
 //
-// What bounds it is shared memory: for 256 rows a 64-wide stage's MMAs take
-// 512 cycles, and a CTA on its own moves 104 KB for them (rows 32 KB in and
-// 32 out, bf16 weights 16 in and 16 out, nibbles 4 and 4), 832 cycles at 128
-// bytes a cycle; it measured 1250.  In a pair each CTA holds half of the rows:
-// 72 KB.  A single CTA remains for calls with few tiles, where pairs would
-// leave SMs without work.
+// In a pair each CTA stages half of the rows, so 64 k of 256 rows x 256
+// features move 72 KB through a CTA's shared memory for 512 cycles of MMAs (a
+// CTA on its own with 256 rows: 104 KB).  A single CTA with 128 rows remains
+// for calls with few tiles, where pairs would leave SMs without work.
 //
-// Both directions read the same packed matrix.  Forward, a stage is 128 rows
-// n x 64 k of it and the bf16 tile is K-major; for the gradient it is 64 rows
-// n x 128 k and the tile's features (k) run along the rows, so the same
-// row-wise expansion writes an MN-major operand: no transpose anywhere.
+// What bounds it otherwise are the hand-offs between the roles: with no
+// copy, expansion or MMA left in it, a 64-wide stage still took 500 to 600
+// cycles.  So a stage is 128 wide (two sub-tiles of one swizzle row each), has
+// one barrier for rows and weights together, and all of its MMAs are issued
+// by an elected thread of a converged warp (from a lane picked by number the
+// operands go through slower registers: 415 against 352 us at
+// 4096x14336x4096).
+//
+// Both directions read the same 128 rows n x 128 k of the packed matrix per
+// stage.  Forward the bf16 sub-tiles are K-major; for the gradient the
+// features (k) run along the rows, so the same row-wise expansion writes an
+// MN-major operand: no transpose anywhere.
 //
 // Roles (768 threads, one CTA per SM, persistent over tiles):
 //   warp 0      rows: tensor copies of 64-wide slices (128-byte swizzle)
@@ -49,28 +55,25 @@ namespace qg {
 namespace {
 
 constexpr int TF = 128;                    // features per CTA and tile
-constexpr int TT = 256;                    // rows per tile at most
-constexpr int KS = 64;                     // reduction per stage: one 128-byte swizzle row
+constexpr int KS = 64;                     // reduction per sub-tile: one 128-byte swizzle row
+constexpr int SUBS = 2;                    // sub-tiles per stage
+constexpr int KST = KS * SUBS;             // reduction per stage
+constexpr int XR = 128;                    // rows per CTA and tile at most
 constexpr int XBOX = 64;                   // rows per tensor copy
-constexpr int NRING = 6;
-constexpr int W_BYTES = TF * KS * 2;       // 16 KiB
-constexpr int NIB_BYTES = TF * KS / 2;     // 4 KiB
+constexpr int STAGES = 3;
+constexpr int NRING = 3;
+constexpr int X_BYTES = XR * KS * 2;       // 16 KiB per sub-tile
+constexpr int W_BYTES = TF * KS * 2;       // 16 KiB per sub-tile
+constexpr int NIB_BYTES = TF * KST / 2;    // 8 KiB per stage
 constexpr int THREADS = 768;
 constexpr int EPI_WARP0 = 4, CONV_WARP0 = 8, CONV_WARPS = 8;  // CONV_WARPS per group
+constexpr int row_tile(bool pair) { return pair ? 2 * XR : XR; }  // rows per tile at most
 
-template <bool PAIR>
-struct Lay {
-  static constexpr int X_BYTES = (PAIR ? TT / 2 : TT) * KS * 2;  // rows of this CTA
-  static constexpr int STAGES = PAIR ? 6 : 4;
-  static constexpr size_t OFF_W = (size_t)STAGES * X_BYTES;
-  static constexpr size_t OFF_N = OFF_W + (size_t)STAGES * W_BYTES;
-  static constexpr size_t OFF_BAR = OFF_N + (size_t)NRING * NIB_BYTES;
-  static constexpr size_t OFF_PRE = OFF_BAR + 512;
-};
-template <bool PAIR>
-size_t tc_smem(int E) {
-  return 1024 + Lay<PAIR>::OFF_PRE + (size_t)(E + 1) * 4;
-}
+constexpr size_t OFF_W = (size_t)STAGES * SUBS * X_BYTES;
+constexpr size_t OFF_N = OFF_W + (size_t)STAGES * SUBS * W_BYTES;
+constexpr size_t OFF_BAR = OFF_N + (size_t)NRING * NIB_BYTES;
+constexpr size_t OFF_PRE = OFF_BAR + 512;
+size_t tc_smem(int E) { return 1024 + OFF_PRE + (size_t)(E + 1) * 4; }
 
 struct TcMaps {
   CUtensorMap nib, rows;
@@ -79,7 +82,7 @@ struct TcMaps {
 struct TcArgs {
   A16W4Call c;
   int F, R;        // features and reduction length
-  int ftiles, stages;
+  int ftiles, stages, subs;  // subs: sub-tiles of the reduction
 };
 
 struct Tile {
@@ -180,7 +183,8 @@ template <>
 struct Scale<QG_W4_F32> {
   uint32_t hi, lo;
 };
-// f32 scales and zeros: s * code + z in f32, rounded to bf16
+// f32 scales and zeros: s * (128 + u) + (z - 136 s) in f32, rounded to bf16
+// (the rounding of z - 136 s is 2^-17 of s at most)
 template <>
 struct Scale<QG_W4_ASYM> {
   float s, z;
@@ -197,36 +201,41 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
   return d;
 }
 
-// Raw stored scale (and zero, zoff bytes further): loaded ahead, turned into
-// a Scale at use.
+// Raw stored scales (and zeros, zoff bytes further) of two neighbouring
+// groups: loaded ahead, turned into a Scale at use.
+struct RawScales {
+  uint2 s, z;  // bf16: both in s.x
+};
 template <int FMT>
-__device__ __forceinline__ uint2 load_scale(const uint8_t* p, int64_t zoff, bool in) {
-  uint2 v = make_uint2(0, 0);
+__device__ __forceinline__ RawScales load_scales(const uint8_t* p, int64_t zoff, bool in) {
+  RawScales v;
+  v.s = v.z = make_uint2(0, 0);
   if (in) {
     if constexpr (FMT == QG_W4_BF16) {
-      v.x = __ldg(reinterpret_cast<const unsigned short*>(p));
+      v.s.x = __ldg(reinterpret_cast<const uint32_t*>(p));
     } else {
-      v.x = __ldg(reinterpret_cast<const uint32_t*>(p));
-      if constexpr (FMT == QG_W4_ASYM) v.y = __ldg(reinterpret_cast<const uint32_t*>(p + zoff));
+      v.s = __ldg(reinterpret_cast<const uint2*>(p));
+      if constexpr (FMT == QG_W4_ASYM) v.z = __ldg(reinterpret_cast<const uint2*>(p + zoff));
     }
   }
   return v;
 }
 template <int FMT>
-__device__ __forceinline__ Scale<FMT> make_scale(uint2 v) {
+__device__ __forceinline__ Scale<FMT> make_scale(const RawScales& v, int i) {
   Scale<FMT> s;
+  const uint32_t raw = i ? v.s.y : v.s.x;
   if constexpr (FMT == QG_W4_BF16) {
-    s.s = v.x | (v.x << 16);
+    s.s = prmt(v.s.x, 0u, i ? 0x3232u : 0x1010u);
   } else if constexpr (FMT == QG_W4_F32) {
-    const float f = __uint_as_float(v.x);
+    const float f = __uint_as_float(raw);
     const uint32_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(f));
     const float rest = f - __uint_as_float(hi << 16);
     const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rn(rest));
     s.hi = hi | (hi << 16);
     s.lo = lo | (lo << 16);
   } else {
-    s.s = __uint_as_float(v.x);
-    s.z = __uint_as_float(v.y);
+    s.s = __uint_as_float(raw);
+    s.z = fmaf(-136.0f, s.s, __uint_as_float(i ? v.z.y : v.z.x));
   }
   return s;
 }
@@ -239,9 +248,9 @@ __device__ __forceinline__ void expand8(uint32_t w, const Scale<FMT>& s, uint32_
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t b = i < 2 ? L : H;
-      // 0x4B0000uu is 2^23 + u
-      const float c0 = __uint_as_float(prmt(b, 0x4B000000u, 0x7440u + (i & 1) * 2)) - 8388616.0f;
-      const float c1 = __uint_as_float(prmt(b, 0x4B000000u, 0x7441u + (i & 1) * 2)) - 8388616.0f;
+      // 0x43uu0000 is 128 + u
+      const float c0 = __uint_as_float(prmt(b, 0x43000000u, (i & 1) ? 0x7244u : 0x7044u));
+      const float c1 = __uint_as_float(prmt(b, 0x43000000u, (i & 1) ? 0x7344u : 0x7144u));
       const float w0 = fmaf(s.s, c0, s.z), w1 = fmaf(s.s, c1, s.z);
       asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(w1), "f"(w0));
     }
@@ -262,13 +271,12 @@ template <int FMT, bool GRAD, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     a16w4_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a,
                     int* status) {
-  using L = Lay<PAIR>;
-  constexpr int STAGES = L::STAGES, X_BYTES = L::X_BYTES;
+  constexpr int TT = row_tile(PAIR);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  const uint32_t sX = smem_u32(smem), sW = smem_u32(smem + L::OFF_W);
-  const uint32_t sN = smem_u32(smem + L::OFF_N);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);  // rows and weights of a stage
+  const uint32_t sX = smem_u32(smem), sW = smem_u32(smem + OFF_W);
+  const uint32_t sN = smem_u32(smem + OFF_N);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // rows and weights of a stage
   uint64_t* empty = full + STAGES;
   uint64_t* n_full = empty + STAGES;
   uint64_t* n_empty = n_full + NRING;
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* t_empty = t_full + 2;
   uint64_t* drain = t_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  int* pre = reinterpret_cast<int*>(smem + L::OFF_PRE);  // [E + 1] row tiles before expert e
+  int* pre = reinterpret_cast<int*>(smem + OFF_PRE);  // [E + 1] row tiles before expert e
 
   const A16W4Call& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0) {
     // ---------------- rows: this CTA's half, or all ----------------
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    uint32_t it = 0;
+    uint32_t it = 0, slot = 0, par = 1;
     bool ok = true;
     for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
@@ -378,20 +386,27 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int mine = PAIR ? n / 2 : n;
       const int y = tl.p0 + (int)rank * mine;
       const int boxes = (mine + XBOX - 1) / XBOX;
+      const uint32_t bytes = (uint32_t)boxes * (XBOX * KS * 2) * (PAIR ? 2u : 1u);
       for (int s = 0; s < stages; ++s, ++it) {
-        const int slot = it % STAGES;
-        if (it >= STAGES) ok = warp_wait(&empty[slot], ((it / STAGES) - 1) & 1, status);
+        ok = warp_wait(&empty[slot], par, status);  // the first round passes
         if (!ok) break;
-        if (lane == 0 && rank == 0)
-          mbar_arrive_expect_tx(&full[slot], (uint32_t)boxes * (XBOX * KS * 2) * (PAIR ? 2u : 1u));
+        const int subs = min(SUBS, a.subs - SUBS * s);
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[slot], bytes * (uint32_t)subs);
+          for (int u = 0; u < subs; ++u)
+            for (int b = 0; b < boxes; ++b) {
+              const uint32_t off = (slot * SUBS + u) * X_BYTES + b * (XBOX * KS * 2);
+              if constexpr (PAIR)
+                tma_load_2d_pair(sX + off, &maps.rows, s * KST + u * KS, y + b * XBOX,
+                                 mapa(smem_u32(&full[slot]), 0));
+              else
+                tma_load_2d(smem + off, &maps.rows, s * KST + u * KS, y + b * XBOX, &full[slot]);
+            }
+        }
         __syncwarp();
-        if (lane < boxes) {
-          const uint32_t dst = sX + slot * X_BYTES + lane * (XBOX * KS * 2);
-          if constexpr (PAIR)
-            tma_load_2d_pair(dst, &maps.rows, s * KS, y + lane * XBOX, mapa(smem_u32(&full[slot]), 0));
-          else
-            tma_load_2d(smem + slot * X_BYTES + lane * (XBOX * KS * 2), &maps.rows, s * KS,
-                        y + lane * XBOX, &full[slot]);
+        if (++slot == STAGES) {
+          slot = 0;
+          par ^= 1;
         }
       }
     }
@@ -402,20 +417,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         warp_wait(&full[k % STAGES], (k / STAGES) & 1, status);
   } else if (warp == 2) {
     // ---------------- nibbles (inputs of the call alone) ----------------
-    uint32_t it = 0;
+    uint32_t it = 0, slot = 0, par = 1;
     bool ok = true;
     for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
       for (int s = 0; s < stages; ++s, ++it) {
-        const int slot = it % NRING;
-        if (it >= NRING) ok = warp_wait(&n_empty[slot], ((it / NRING) - 1) & 1, status);
+        ok = warp_wait(&n_empty[slot], par, status);  // the first round passes
         if (!ok) break;
-        if (lane == 0) {
+        if (elect_one()) {
           mbar_arrive_expect_tx(&n_full[slot], NIB_BYTES);
-          if (GRAD) tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, tl.f0 / 8, s * KS, tl.e, &n_full[slot]);
-          else tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, s * (KS / 8), tl.f0, tl.e, &n_full[slot]);
+          if (GRAD) tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, tl.f0 / 8, s * KST, tl.e, &n_full[slot]);
+          else tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, s * (KST / 8), tl.f0, tl.e, &n_full[slot]);
         }
         __syncwarp();
+        if (++slot == NRING) {
+          slot = 0;
+          par ^= 1;
+        }
       }
     }
     for (uint32_t k = it > NRING ? it - NRING : 0; k < it; ++k)
@@ -441,14 +459,22 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], par, status));
           if (!ok) break;
           tc_fence_after();
+          const int subs = min(SUBS, a.subs - SUBS * s);
           if (elect_one()) {
             // descriptor addresses count 16 bytes: 16 k further is 32 bytes
             // of a K-major row, or 16 rows of 128 bytes of the MN-major tile
-            const uint64_t dx = sdesc_sw128(sX + slot * X_BYTES);
-            const uint64_t dw = GRAD ? sdesc_mn_sw128(sW + slot * W_BYTES) : sdesc_sw128(sW + slot * W_BYTES);
+            uint64_t dx = sdesc_sw128(sX + slot * (SUBS * X_BYTES));
+            const uint32_t w0 = sW + slot * (SUBS * W_BYTES);
+            uint64_t dw = GRAD ? sdesc_mn_sw128(w0) : sdesc_sw128(w0);
 #pragma unroll
-            for (int k = 0; k < KS / 16; ++k)
-              mma_f16<PAIR>(d, dw + (GRAD ? 128 : 2) * k, dx + 2 * k, idesc, s > 0 || k > 0);
+            for (int u = 0; u < SUBS; ++u) {
+              if (u >= subs) break;
+#pragma unroll
+              for (int k = 0; k < KS / 16; ++k)
+                mma_f16<PAIR>(d, dw + (GRAD ? 128 : 2) * k, dx + 2 * k, idesc, s > 0 || u > 0 || k > 0);
+              dx += X_BYTES >> 4;
+              dw += W_BYTES >> 4;
+            }
             commit<PAIR>(&empty[slot]);
             if (s == stages - 1) commit<PAIR>(&t_full[buf]);
           }
@@ -469,58 +495,66 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---------------- expansion ----------------
     const uint32_t group = (uint32_t)(warp - CONV_WARP0) / CONV_WARPS;
     const int tid = (threadIdx.x - CONV_WARP0 * 32) % (CONV_WARPS * 32);
-    // forward: row n (of 128), half of its 64 k; gradient: row n (of 64),
-    // quarter of its 128 k.  32 weights, one group, 16 nibble bytes each.
-    const int row = GRAD ? tid >> 2 : tid >> 1, part = GRAD ? tid & 3 : tid & 1;
-    const uint32_t nib_at = (uint32_t)(tid * 16);
+    // row n of the stage's 128, and half of its 128 k: 64 weights, two groups,
+    // 32 nibble bytes.  Forward, the halves are the stage's sub-tiles (K-major
+    // rows); for the gradient the rows' halves are, and this half of k is a
+    // block of 64 features (MN-major).
+    const int row = tid >> 1, half = tid & 1;
+    const uint32_t nib_at = (uint32_t)(tid * 32);
     const int G = c.K >> 5;
     constexpr int SB = FMT == QG_W4_BF16 ? 2 : 4;
     const int64_t zoff = (int64_t)c.N * G * 4;
-    // gradient: parts 2 and 3 go 8 KiB behind 0 and 1, to the same banks, so
-    // they store their words in the order 2, 3, 0, 1
-    const bool turn = GRAD && part >= 2;
-    const int c0 = GRAD ? (part & 1) * 4 + (turn ? 2 : 0) : part * 4;
-    const uint32_t w_at = sW + (GRAD ? (part >> 1) * 8192 + row * 128 : row * 128);
-    const uint32_t step_b = GRAD ? (uint32_t)(KS * G * SB) : 2u * SB;  // scales: stage to stage
+    const uint32_t w_at = sW + (GRAD ? (row >> 6) * W_BYTES + half * 8192 + (row & 63) * 128
+                                     : half * W_BYTES + row * 128);
+    const uint32_t turn = (uint32_t)((row & 7) ^ (half << 2));  // swizzle, and the groups' order
+    const uint32_t step_b = GRAD ? (uint32_t)(KST * G * SB) : 4u * SB;  // scales: stage to stage
     uint32_t it = 0, slot = group, ns = group;
     uint32_t par = 1, npar = 0;  // parities of the waits for a free slot and for nibbles
     bool ok = true;
     for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
       const uint8_t* scl = c.packed + (int64_t)tl.e * c.expert_bytes + (int64_t)c.N * (c.K >> 1);
-      const int g = GRAD ? (tl.f0 >> 5) + part : part;
-      const int n0 = GRAD ? row : tl.f0 + row;
+      const int g = (GRAD ? tl.f0 >> 5 : 0) + 2 * half;  // forward: 4 further with every stage
+      const int n0 = GRAD ? row : tl.f0 + row;           // gradient: 128 further
       scl += ((int64_t)n0 * G + g) * SB;
-      // rows of W from this one on (gradient: 64 further with every stage)
-      const int left = GRAD && g >= G ? 0 : c.N - n0;
-      auto fetch = [&](int s) {
-        return load_scale<FMT>(scl + (int64_t)s * step_b, zoff, s < stages && (GRAD ? KS * s : 0) < left);
-      };
+      // stages of this tile in which the thread's weights exist
+      const int live = GRAD ? (g < G ? (c.N - n0 + KST - 1) / KST : 0) : (n0 < c.N ? (G - g + 3) / 4 : 0);
+      auto fetch = [&](int s) { return load_scales<FMT>(scl + (int64_t)s * step_b, zoff, s < live); };
       int s = (it & 1) == group ? 0 : 1;  // this group's stages: every other one
-      uint2 now = fetch(s), next = fetch(s + 2);
+      RawScales now = fetch(s);
       for (; s < stages; s += 2) {
         ok = warp_wait(&n_full[ns], npar, status);
         if (!ok) break;
-        uint4 q;
+        uint32_t wd[8];
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                     : "=r"(wd[0]), "=r"(wd[1]), "=r"(wd[2]), "=r"(wd[3])
                      : "r"(sN + ns * NIB_BYTES + nib_at)
                      : "memory");
-        const Scale<FMT> sc = make_scale<FMT>(now);
-        now = next;
-        next = fetch(s + 4);
-        const uint32_t wd[4] = {turn ? q.z : q.x, turn ? q.w : q.y, turn ? q.x : q.z, turn ? q.y : q.w};
-        uint32_t o[4][4];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(wd[4]), "=r"(wd[5]), "=r"(wd[6]), "=r"(wd[7])
+                     : "r"(sN + ns * NIB_BYTES + nib_at + 16)
+                     : "memory");
+        // the halves' 16-byte parts lie in the same banks: the second half
+        // stores its second group first
+        const Scale<FMT> sc[2] = {make_scale<FMT>(now, half), make_scale<FMT>(now, half ^ 1)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) expand8<FMT>(wd[i], sc, o[i]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = wd[i], a1 = wd[4 + i];
+          wd[i] = half ? a1 : a0;
+          wd[4 + i] = half ? a0 : a1;
+        }
+        now = fetch(s + 2);
         ok = warp_wait(&empty[slot], par, status);  // the first round passes
         if (!ok) break;
-        const uint32_t dst = w_at + slot * W_BYTES;
+        const uint32_t dst = w_at + slot * (SUBS * W_BYTES);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (((c0 ^ i) ^ (row & 7)) << 4)),
-                       "r"(o[i][0]), "r"(o[i][1]), "r"(o[i][2]), "r"(o[i][3])
+        for (int i = 0; i < 8; ++i) {
+          uint32_t o[4];
+          expand8<FMT>(wd[i], sc[i >> 2], o);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + ((i ^ turn) << 4)),
+                       "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                        : "memory");
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -671,7 +705,7 @@ int a16w4_tc_setup() {
   for (int fmt = 0; fmt < 3; ++fmt)
     for (int v = 0; v < 4; ++v) {
       const bool pair = v & 1;
-      const size_t most = pair ? tc_smem<true>(kA16W4MaxExperts) : tc_smem<false>(kA16W4MaxExperts);
+      const size_t most = tc_smem(kA16W4MaxExperts);
       if (cudaFuncSetAttribute(kernel_of(fmt, v >= 2, pair), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)most) != cudaSuccess)
         return QG_ERR_CUDA;
@@ -683,7 +717,7 @@ int a16w4_tc_setup() {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = tc_smem<true>(kA16W4MaxExperts);
+  cfg.dynamicSmemBytes = tc_smem(kA16W4MaxExperts);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -729,20 +763,20 @@ int launch_a16w4_tc(const A16W4Call& call, bool grad, void* ws, cudaStream_t st)
   a.c = c;
   a.F = grad ? c.K : c.N;
   a.R = grad ? c.N : c.K;
-  a.stages = (int)cdiv(a.R, KS);
-  // at most this many tiles of rows: every expert's last one may be partial
-  const int64_t row_tiles = c.offsets ? cdiv(c.S, TT) + min64(c.E, c.S) : cdiv(c.S, TT);
+  a.subs = (int)cdiv(a.R, KS);
+  a.stages = (int)cdiv(a.subs, SUBS);
   // pairs, unless their tiles leave half of the SMs without work
-  const int64_t likely = c.offsets ? max64(cdiv(c.S, TT), min64(c.E, c.S)) : row_tiles;
+  const int64_t likely = c.offsets ? max64(cdiv(c.S, row_tile(true)), min64(c.E, c.S)) : cdiv(c.S, row_tile(true));
   const bool pair = likely * cdiv(a.F, 2 * TF) * 4 > num_sms();
+  // at most this many tiles of rows: every expert's last one may be partial
+  const int64_t row_tiles = cdiv(c.S, row_tile(pair)) + (c.offsets ? min64(c.E, c.S) : 0);
   a.ftiles = (int)cdiv(a.F, pair ? 2 * TF : TF);
   TcMaps m;
   {
     cuuint64_t dims[3] = {(cuuint64_t)c.K / 8, (cuuint64_t)c.N, (cuuint64_t)c.E};
     cuuint64_t strides[2] = {(cuuint64_t)c.K / 2,
                              (cuuint64_t)(c.E > 1 ? c.expert_bytes : (int64_t)c.N * (c.K / 2))};
-    cuuint32_t box[3] = {grad ? (cuuint32_t)TF / 8 : (cuuint32_t)KS / 8,
-                         grad ? (cuuint32_t)KS : (cuuint32_t)TF, 1};
+    cuuint32_t box[3] = {KST / 8, TF, 1};  // 128 k of 128 rows in both directions
     cuuint32_t es[3] = {1, 1, 1};
     if (g_tc_encode(&m.nib, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, (void*)c.packed, dims, strides, box, es,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -764,7 +798,7 @@ int launch_a16w4_tc(const A16W4Call& call, bool grad, void* ws, cudaStream_t st)
   const int64_t most = row_tiles * a.ftiles;
   cfg.gridDim = dim3(pair ? 2 * (unsigned)min64(g_tc_pairs[dev], most) : (unsigned)min64(num_sms(), most));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = pair ? tc_smem<true>(c.E) : tc_smem<false>(c.E);
+  cfg.dynamicSmemBytes = tc_smem(c.E);
   if (pair) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
