@@ -694,9 +694,10 @@ int64_t packed_bytes(int N, int K, int format) {
 }
 
 // Few rows per expert stream the weights past warp MMAs, more go to the
-// tensor cores: 16 rows at N = 14336, K = 4096 take 19 us here and 26 there,
-// 32 rows 34 (in blocks of 32) and 26.
-bool few_rows(int E, int S) { return cdiv(S, E) <= 16; }
+// tensor cores.  One matrix: 16 rows at N = 14336, K = 4096 take 19 us here
+// and 23 there, 32 rows 34 and 24.  Experts (64 of 2048 x 2048): 4 rows each
+// take 62 us both ways, 16 rows 122 and 85.
+bool few_rows(int E, int S) { return cdiv(S, E) <= (E > 1 ? 4 : 16); }
 
 // Checks of every product: QG_OK when the call can run (S may be 0).
 int product_args(int E, int S, int N, int K, const void* in, int64_t ld_in, int in_cols,

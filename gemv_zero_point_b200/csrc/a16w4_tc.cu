@@ -73,6 +73,8 @@ constexpr size_t OFF_W = (size_t)STAGES * SUBS * X_BYTES;
 constexpr size_t OFF_N = OFF_W + (size_t)STAGES * SUBS * W_BYTES;
 constexpr size_t OFF_BAR = OFF_N + (size_t)NRING * NIB_BYTES;
 constexpr size_t OFF_PRE = OFF_BAR + 512;
+constexpr int PART_LD = TF + 4;            // floats per row of a partial tile
+static_assert((size_t)XR * PART_LD * 4 <= OFF_N, "partial tiles reuse the stages");
 size_t tc_smem(int E) { return 1024 + OFF_PRE + (size_t)(E + 1) * 4; }
 
 struct TcMaps {
@@ -83,6 +85,7 @@ struct TcArgs {
   A16W4Call c;
   int F, R;        // features and reduction length
   int ftiles, stages, subs;  // subs: sub-tiles of the reduction
+  int splits;        // kShared: CTAs of a cluster
 };
 
 struct Tile {
@@ -267,10 +270,15 @@ __device__ __forceinline__ void expand8(uint32_t w, const Scale<FMT>& s, uint32_
   }
 }
 
-template <int FMT, bool GRAD, bool PAIR>
+// How CTAs share a tile: on its own, a pair (256 features, cta_group::2), or a
+// cluster of `splits` CTAs that share its reduction.
+enum TcMode { kSingle = 0, kPair = 1, kShared = 2 };
+
+template <int FMT, bool GRAD, int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
     a16w4_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a,
                     int* status) {
+  constexpr bool PAIR = MODE == kPair, SHARED = MODE == kShared;
   constexpr int TT = row_tile(PAIR);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -285,11 +293,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* drain = t_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* pre = reinterpret_cast<int*>(smem + OFF_PRE);  // [E + 1] row tiles before expert e
+  float* part = reinterpret_cast<float*>(smem);        // shared reduction: [row][PART_LD]
 
   const A16W4Call& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0;  // rank 0 issues the pair's MMAs
-  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int splits = SHARED ? a.splits : 1, split = SHARED ? (int)cluster_rank() : 0;
+  const int first = PAIR ? blockIdx.x >> 1 : SHARED ? blockIdx.x / splits : blockIdx.x;
+  const int step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
@@ -351,7 +362,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int64_t total = (int64_t)pre[c.E] * a.ftiles;
-  const int stages = a.stages;
+  // this CTA's part of the reduction, in stages
+  const int all_stages = a.stages;
+  const int s_first = SHARED ? all_stages * split / splits : 0;
+  const int stages = SHARED ? all_stages * (split + 1) / splits - s_first : all_stages;
 
   constexpr int kRowStep = PAIR ? 32 : 16;  // MMA N in steps of 16 per CTA
   // tile t: features fastest, so concurrent CTAs share the rows' tiles
@@ -390,17 +404,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int s = 0; s < stages; ++s, ++it) {
         ok = warp_wait(&empty[slot], par, status);  // the first round passes
         if (!ok) break;
-        const int subs = min(SUBS, a.subs - SUBS * s);
+        const int subs = min(SUBS, a.subs - SUBS * (s_first + s));
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[slot], bytes * (uint32_t)subs);
           for (int u = 0; u < subs; ++u)
             for (int b = 0; b < boxes; ++b) {
               const uint32_t off = (slot * SUBS + u) * X_BYTES + b * (XBOX * KS * 2);
               if constexpr (PAIR)
-                tma_load_2d_pair(sX + off, &maps.rows, s * KST + u * KS, y + b * XBOX,
+                tma_load_2d_pair(sX + off, &maps.rows, (s_first + s) * KST + u * KS, y + b * XBOX,
                                  mapa(smem_u32(&full[slot]), 0));
               else
-                tma_load_2d(smem + off, &maps.rows, s * KST + u * KS, y + b * XBOX, &full[slot]);
+                tma_load_2d(smem + off, &maps.rows, (s_first + s) * KST + u * KS, y + b * XBOX, &full[slot]);
             }
         }
         __syncwarp();
@@ -426,8 +440,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&n_full[slot], NIB_BYTES);
-          if (GRAD) tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, tl.f0 / 8, s * KST, tl.e, &n_full[slot]);
-          else tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, s * (KST / 8), tl.f0, tl.e, &n_full[slot]);
+          if (GRAD) tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, tl.f0 / 8, (s_first + s) * KST, tl.e, &n_full[slot]);
+          else tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, (s_first + s) * (KST / 8), tl.f0, tl.e, &n_full[slot]);
         }
         __syncwarp();
         if (++slot == NRING) {
@@ -459,7 +473,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], par, status));
           if (!ok) break;
           tc_fence_after();
-          const int subs = min(SUBS, a.subs - SUBS * s);
+          const int subs = min(SUBS, a.subs - SUBS * (s_first + s));
           if (elect_one()) {
             // descriptor addresses count 16 bytes: 16 k further is 32 bytes
             // of a K-major row, or 16 rows of 128 bytes of the MN-major tile
@@ -519,7 +533,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       scl += ((int64_t)n0 * G + g) * SB;
       // stages of this tile in which the thread's weights exist
       const int live = GRAD ? (g < G ? (c.N - n0 + KST - 1) / KST : 0) : (n0 < c.N ? (G - g + 3) / 4 : 0);
-      auto fetch = [&](int s) { return load_scales<FMT>(scl + (int64_t)s * step_b, zoff, s < live); };
+      auto fetch = [&](int s) {
+        return load_scales<FMT>(scl + (int64_t)(s_first + s) * step_b, zoff, s_first + s < live);
+      };
       int s = (it & 1) == group ? 0 : 1;  // this group's stages: every other one
       RawScales now = fetch(s);
       for (; s < stages; s += 2) {
@@ -592,7 +608,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t v[32];
         tmem_ld32(tmem_base + ((uint32_t)(32 * q) << 16) + buf * TT + j0, v);
         tmem_wait_ld();
-        if (vec) {
+        if constexpr (SHARED) {
+          // partial sums over the stages' memory: every MMA has ended
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j0 + j < tl.np) part[(j0 + j) * PART_LD + 32 * q + lane] = __uint_as_float(v[j]);
+        } else if (vec) {
           // lanes f, f + 1 swap halves: the even one stores both features of
           // row j, the odd one those of row j + 1
 #pragma unroll
@@ -627,6 +648,45 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
 
+  if constexpr (SHARED) {
+    // Sum the cluster's partial tiles, each CTA its part of the rows, in the
+    // order of the ranks.
+    __syncwarp();
+    cluster_sync_all();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Tile tl = tile_at(first);
+    const uint32_t base = smem_u32(part);
+    const int j0 = tl.np * split / splits, j1 = tl.np * (split + 1) / splits;
+    const int f = (int)(threadIdx.x & 63) * 2;  // two features
+    const bool two = tl.f0 + f + 1 < a.F;
+    float b0 = 0.0f, b1 = 0.0f;
+    if (c.bias && tl.f0 + f < a.F) b0 = __ldg(c.bias + tl.f0 + f);
+    if (c.bias && two) b1 = __ldg(c.bias + tl.f0 + f + 1);
+    const bool vec = ((reinterpret_cast<uintptr_t>(c.out) & 3) == 0) && ((c.ld_out & 1) == 0);
+    for (int j = j0 + (int)(threadIdx.x >> 6); j < j1; j += THREADS / 64) {
+      float s0 = b0, s1 = b1;
+      for (int k = 0; k < splits; ++k) {
+        float x, y;
+        asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+                     : "=f"(x), "=f"(y)
+                     : "r"(mapa(base + (uint32_t)(j * PART_LD + f) * 4, (uint32_t)k))
+                     : "memory");
+        s0 += x;
+        s1 += y;
+      }
+      uint16_t* dst = c.out + (int64_t)(tl.p0 + j) * c.ld_out + tl.f0 + f;
+      const uint16_t h0 = __bfloat16_as_ushort(__float2bfloat16_rn(s0));
+      const uint16_t h1 = __bfloat16_as_ushort(__float2bfloat16_rn(s1));
+      if (vec && two) {
+        *reinterpret_cast<uint32_t*>(dst) = h0 | ((uint32_t)h1 << 16);
+      } else {
+        if (tl.f0 + f < a.F) dst[0] = h0;
+        if (two) dst[1] = h1;
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA ends while another may read its sums
+  }
   // no CTA of a pair leaves while the other may still signal its barriers or
   // read its shared memory
   __syncwarp();
@@ -678,15 +738,18 @@ __global__ void __launch_bounds__(256) a16w4_gather_kernel(const __grid_constant
 // ---------------------------------------------------------------------------
 PFN_cuTensorMapEncodeTiled_v12000 g_tc_encode = nullptr;
 
-template <int FMT>
-const void* kernel_of(bool grad, bool pair) {
-  if (grad) return pair ? (const void*)a16w4_tc_kernel<FMT, true, true> : (const void*)a16w4_tc_kernel<FMT, true, false>;
-  return pair ? (const void*)a16w4_tc_kernel<FMT, false, true> : (const void*)a16w4_tc_kernel<FMT, false, false>;
+template <int FMT, bool GRAD>
+const void* kernel_of(int mode) {
+  if (mode == kPair) return (const void*)a16w4_tc_kernel<FMT, GRAD, kPair>;
+  if (mode == kShared) return (const void*)a16w4_tc_kernel<FMT, GRAD, kShared>;
+  return (const void*)a16w4_tc_kernel<FMT, GRAD, kSingle>;
 }
-const void* kernel_of(int fmt, bool grad, bool pair) {
-  if (fmt == QG_W4_F32) return kernel_of<QG_W4_F32>(grad, pair);
-  if (fmt == QG_W4_BF16) return kernel_of<QG_W4_BF16>(grad, pair);
-  return kernel_of<QG_W4_ASYM>(grad, pair);
+const void* kernel_of(int fmt, bool grad, int mode) {
+  if (fmt == QG_W4_F32)
+    return grad ? kernel_of<QG_W4_F32, true>(mode) : kernel_of<QG_W4_F32, false>(mode);
+  if (fmt == QG_W4_BF16)
+    return grad ? kernel_of<QG_W4_BF16, true>(mode) : kernel_of<QG_W4_BF16, false>(mode);
+  return grad ? kernel_of<QG_W4_ASYM, true>(mode) : kernel_of<QG_W4_ASYM, false>(mode);
 }
 
 constexpr int kMaxDevices = 64;
@@ -703,13 +766,10 @@ int a16w4_tc_setup() {
     return QG_ERR_CUDA;
   g_tc_encode = (PFN_cuTensorMapEncodeTiled_v12000)fn;
   for (int fmt = 0; fmt < 3; ++fmt)
-    for (int v = 0; v < 4; ++v) {
-      const bool pair = v & 1;
-      const size_t most = tc_smem(kA16W4MaxExperts);
-      if (cudaFuncSetAttribute(kernel_of(fmt, v >= 2, pair), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)most) != cudaSuccess)
+    for (int v = 0; v < 6; ++v)
+      if (cudaFuncSetAttribute(kernel_of(fmt, v >= 3, v % 3), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)tc_smem(kA16W4MaxExperts)) != cudaSuccess)
         return QG_ERR_CUDA;
-    }
   // how many pairs can be resident at once (an SM whose partner is disabled
   // cannot host one)
   int dev = 0;
@@ -726,7 +786,7 @@ int a16w4_tc_setup() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int pairs = 0;
-  if (cudaOccupancyMaxActiveClusters(&pairs, kernel_of(QG_W4_F32, false, true), &cfg) != cudaSuccess ||
+  if (cudaOccupancyMaxActiveClusters(&pairs, kernel_of(QG_W4_F32, false, kPair), &cfg) != cudaSuccess ||
       pairs < 1)
     return QG_ERR_CUDA;
   g_tc_pairs[dev] = pairs;
@@ -796,18 +856,24 @@ int launch_a16w4_tc(const A16W4Call& call, bool grad, void* ws, cudaStream_t st)
       return QG_ERR_CUDA;
   }
   const int64_t most = row_tiles * a.ftiles;
-  cfg.gridDim = dim3(pair ? 2 * (unsigned)min64(g_tc_pairs[dev], most) : (unsigned)min64(num_sms(), most));
+  // A dense call whose tiles leave SMs without work: clusters share each
+  // tile's reduction, two stages or more per CTA.
+  a.splits = 1;
+  if (!pair && !c.offsets)
+    while (a.splits < 8 && most * a.splits * 2 <= num_sms() && a.stages >= 4 * a.splits)
+      a.splits *= 2;
+  cfg.gridDim = dim3(pair ? 2 * (unsigned)min64(g_tc_pairs[dev], most) : (unsigned)(a.splits > 1 ? most * a.splits : min64(num_sms(), most)));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = tc_smem(c.E);
-  if (pair) {
+  if (pair || a.splits > 1) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = pair ? 2 : (unsigned)a.splits;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
   void* args[] = {&m, &a, &status};
-  return cudaLaunchKernelExC(&cfg, kernel_of(c.format, grad, pair), args) == cudaSuccess ? QG_OK
+  return cudaLaunchKernelExC(&cfg, kernel_of(c.format, grad, pair ? kPair : a.splits > 1 ? kShared : kSingle), args) == cudaSuccess ? QG_OK
                                                                                         : QG_ERR_CUDA;
 }
 
