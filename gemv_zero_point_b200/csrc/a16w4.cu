@@ -113,13 +113,6 @@ __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&p)[4]) {
   p[3] = prmt(H, 0x43434343u, 0x5342u);
 }
 
-// L2 prefetch of the 16-byte-aligned interior of [p, p + bytes).
-__device__ __forceinline__ void prefetch_l2(const void* p, int64_t bytes) {
-  const uintptr_t b = ((uintptr_t)p + 15) & ~(uintptr_t)15;
-  const uintptr_t e = ((uintptr_t)p + (uintptr_t)bytes) & ~(uintptr_t)15;
-  if (e > b) bulk_prefetch_l2((const void*)b, (uint32_t)(e - b));
-}
-
 // q = v / d and the rest r, by 32-bit division where v allows it.
 __device__ __forceinline__ void divide(int64_t v, int d, int64_t& q, int64_t& r) {
   if (v <= 0x7FFFFFFF) {

@@ -65,6 +65,7 @@ constexpr int NRING = 3;
 constexpr int X_BYTES = XR * KS * 2;       // 16 KiB per sub-tile
 constexpr int W_BYTES = TF * KS * 2;       // 16 KiB per sub-tile
 constexpr int NIB_BYTES = TF * KST / 2;    // 8 KiB per stage
+constexpr int kFewRows = 64;               // rows of a tile up to which its weights' bytes count
 constexpr int THREADS = 768;
 constexpr int EPI_WARP0 = 4, CONV_WARP0 = 8, CONV_WARPS = 8;  // CONV_WARPS per group
 constexpr int row_tile(bool pair) { return pair ? 2 * XR : XR; }  // rows per tile at most
@@ -435,6 +436,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
+      // With few rows the weights' bytes count: the next tile's into L2 (its
+      // 128 rows lie together; the gradient's tiles are columns).
+      if (!GRAD && t + step < total) {
+        const Tile nx = tile_at(t + step);
+        if (nx.np <= kFewRows && elect_one()) {
+          const int rows = min(TF, c.N - nx.f0), G = c.K >> 5;
+          const uint8_t* w = c.packed + (int64_t)nx.e * c.expert_bytes;
+          constexpr int sb = FMT == QG_W4_BF16 ? 2 : 4;
+          if (rows > 0) {
+            prefetch_l2(w + (int64_t)nx.f0 * (c.K >> 1), (int64_t)rows * (c.K >> 1));
+            w += (int64_t)c.N * (c.K >> 1) + (int64_t)nx.f0 * G * sb;
+            prefetch_l2(w, (int64_t)rows * G * sb);
+            if (FMT == QG_W4_ASYM) prefetch_l2(w + (int64_t)c.N * G * 4, (int64_t)rows * G * sb);
+          }
+        }
+        __syncwarp();
+      }
       for (int s = 0; s < stages; ++s, ++it) {
         ok = warp_wait(&n_empty[slot], par, status);  // the first round passes
         if (!ok) break;
@@ -537,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         return load_scales<FMT>(scl + (int64_t)(s_first + s) * step_b, zoff, s_first + s < live);
       };
       int s = (it & 1) == group ? 0 : 1;  // this group's stages: every other one
-      RawScales now = fetch(s);
+      RawScales now = fetch(s), next = fetch(s + 2);
       for (; s < stages; s += 2) {
         ok = warp_wait(&n_full[ns], npar, status);
         if (!ok) break;
@@ -559,7 +577,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           wd[i] = half ? a1 : a0;
           wd[4 + i] = half ? a0 : a1;
         }
-        now = fetch(s + 2);
+        now = next;
+        next = fetch(s + 4);
         ok = warp_wait(&empty[slot], par, status);  // the first round passes
         if (!ok) break;
         const uint32_t dst = w_at + slot * (SUBS * W_BYTES);
@@ -595,6 +614,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const bool even = (lane & 1) == 0;
     const bool vec = ((reinterpret_cast<uintptr_t>(c.out) & 3) == 0) && ((c.ld_out & 1) == 0);
+    const bool vec4 = ((reinterpret_cast<uintptr_t>(c.out) & 7) == 0) && ((c.ld_out & 3) == 0);
     uint32_t use = 0;
     for (int64_t t = first; t < total; t += step, ++use) {
       const Tile tl = tile_at(t);
@@ -613,6 +633,32 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (j0 + j < tl.np) part[(j0 + j) * PART_LD + 32 * q + lane] = __uint_as_float(v[j]);
+        } else if (vec4 && tl.f0 + 32 * q + 32 <= a.F) {
+          // A quad's lanes hold 4 rows j .. j + 3 of 4 features; two swaps
+          // give each lane one row of all four.
+          const int jl = j0 + (lane & 1) + (lane & 2);  // this lane's row of the four
+          uint16_t* dst = c.out + (int64_t)(tl.p0 + jl) * c.ld_out + (f & ~3);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            if (j0 + j >= tl.np) break;
+            uint32_t lo, hi;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                : "=r"(lo)
+                : "f"(__uint_as_float(v[j + 1]) + b), "f"(__uint_as_float(v[j]) + b));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                : "=r"(hi)
+                : "f"(__uint_as_float(v[j + 3]) + b), "f"(__uint_as_float(v[j + 2]) + b));
+            // features f, f + 1 of rows j (even lanes) or j + 1 (odd), and 2 further
+            const uint32_t lo2 = __shfl_xor_sync(0xffffffffu, lo, 1);
+            const uint32_t hi2 = __shfl_xor_sync(0xffffffffu, hi, 1);
+            const uint32_t x = even ? prmt(lo, lo2, 0x5410) : prmt(lo2, lo, 0x7632);
+            const uint32_t y = even ? prmt(hi, hi2, 0x5410) : prmt(hi2, hi, 0x7632);
+            const bool first_pair = (lane & 2) == 0;
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, first_pair ? y : x, 2);
+            if (jl + j < tl.np)
+              *reinterpret_cast<uint2*>(dst) = first_pair ? make_uint2(x, other) : make_uint2(other, y);
+            dst += 4 * c.ld_out;
+          }
         } else if (vec) {
           // lanes f, f + 1 swap halves: the even one stores both features of
           // row j, the odd one those of row j + 1
