@@ -59,7 +59,12 @@ constexpr int KS = 64;                     // reduction per sub-tile: one 128-by
 constexpr int SUBS = 2;                    // sub-tiles per stage
 constexpr int KST = KS * SUBS;             // reduction per stage
 constexpr int XR = 128;                    // rows per CTA and tile at most
-constexpr int XBOX = 64;                   // rows per tensor copy
+// Rows per tensor copy: the smallest of these that holds a CTA's rows.  One
+// copy takes the copy engine some 350 cycles whatever its size, so a stage is
+// one copy: both sub-tiles of all rows.
+constexpr int kBoxes = 3;
+__host__ __device__ constexpr int box_rows(int i) { return 32 << i; }
+__device__ __forceinline__ int box_of(int rows) { return rows <= 32 ? 0 : rows <= 64 ? 1 : 2; }
 constexpr int STAGES = 3;
 constexpr int NRING = 3;
 constexpr int X_BYTES = XR * KS * 2;       // 16 KiB per sub-tile
@@ -79,7 +84,7 @@ static_assert((size_t)XR * PART_LD * 4 <= OFF_N, "partial tiles reuse the stages
 size_t tc_smem(int E) { return 1024 + OFF_PRE + (size_t)(E + 1) * 4; }
 
 struct TcMaps {
-  CUtensorMap nib, rows;
+  CUtensorMap nib, rows[kBoxes];
 };
 
 struct TcArgs {
@@ -87,6 +92,7 @@ struct TcArgs {
   int F, R;        // features and reduction length
   int ftiles, stages, subs;  // subs: sub-tiles of the reduction
   int splits;        // kShared: CTAs of a cluster
+  int whole;         // the reduction is whole sub-tiles: rows as [64-wide block][row][64]
 };
 
 struct Tile {
@@ -137,15 +143,38 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
-// Tensor load that completes on the barrier at cluster address `bar`, which
-// may be the other CTA's (no multicast).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int x, int y,
-                                                 uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(bar)
-      : "memory");
+// Tensor loads of rows; in a pair they complete on the barrier at cluster
+// address `bar`, which may be the other CTA's (no multicast).
+template <bool PAIR>
+__device__ __forceinline__ void load_rows_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void load_rows_3d(uint32_t dst, const void* tmap, int y, int block,
+                                             uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(0), "r"(y), "r"(block), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(0), "r"(y), "r"(block), "r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
@@ -320,7 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(drain, 1);
     fence_mbar_init();
     prefetch_tmap(&maps.nib);
-    prefetch_tmap(&maps.rows);
+    for (int b = 0; b < kBoxes; ++b) prefetch_tmap(&maps.rows[b]);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -400,23 +429,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int n = (tl.np + kRowStep - 1) & ~(kRowStep - 1);
       const int mine = PAIR ? n / 2 : n;
       const int y = tl.p0 + (int)rank * mine;
-      const int boxes = (mine + XBOX - 1) / XBOX;
-      const uint32_t bytes = (uint32_t)boxes * (XBOX * KS * 2) * (PAIR ? 2u : 1u);
+      const int box = box_of(mine);
+      const uint32_t sub_b = (uint32_t)box_rows(box) * (KS * 2);  // bytes of a sub-tile
+      const void* map = &maps.rows[box];
       for (int s = 0; s < stages; ++s, ++it) {
         ok = warp_wait(&empty[slot], par, status);  // the first round passes
         if (!ok) break;
-        const int subs = min(SUBS, a.subs - SUBS * (s_first + s));
+        const int subs = a.whole ? SUBS : min(SUBS, a.subs - SUBS * (s_first + s));
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(&full[slot], bytes * (uint32_t)subs);
-          for (int u = 0; u < subs; ++u)
-            for (int b = 0; b < boxes; ++b) {
-              const uint32_t off = (slot * SUBS + u) * X_BYTES + b * (XBOX * KS * 2);
-              if constexpr (PAIR)
-                tma_load_2d_pair(sX + off, &maps.rows, (s_first + s) * KST + u * KS, y + b * XBOX,
-                                 mapa(smem_u32(&full[slot]), 0));
-              else
-                tma_load_2d(smem + off, &maps.rows, (s_first + s) * KST + u * KS, y + b * XBOX, &full[slot]);
-            }
+          if (rank == 0) mbar_arrive_expect_tx(&full[slot], sub_b * (uint32_t)(PAIR ? 2 * subs : subs));
+          const uint32_t dst = sX + slot * (SUBS * X_BYTES);
+          const uint32_t bar = PAIR ? mapa(smem_u32(&full[slot]), 0) : smem_u32(&full[slot]);
+          if (a.whole) {
+            load_rows_3d<PAIR>(dst, map, y, SUBS * (s_first + s), bar);
+          } else {
+            for (int u = 0; u < subs; ++u)
+              load_rows_2d<PAIR>(dst + u * sub_b, map, (s_first + s) * KST + u * KS, y, bar);
+          }
         }
         __syncwarp();
         if (++slot == STAGES) {
@@ -485,6 +514,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                ((uint32_t)(n >> 3) << 17) |
                                ((uint32_t)((PAIR ? 2 * TF : TF) >> 4) << 24);
         const uint32_t buf = use & 1;
+        const uint32_t next_x = (uint32_t)box_rows(box_of(PAIR ? n / 2 : n)) * (KS * 2) >> 4;
         ok = warp_wait(&t_empty[buf], ((use >> 1) & 1) ^ 1, status);
         const uint32_t d = tmem_base + buf * TT;
         for (int s = 0; s < stages && ok; ++s) {
@@ -504,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int k = 0; k < KS / 16; ++k)
                 mma_f16<PAIR>(d, dw + (GRAD ? 128 : 2) * k, dx + 2 * k, idesc, s > 0 || u > 0 || k > 0);
-              dx += X_BYTES >> 4;
+              dx += next_x;
               dw += W_BYTES >> 4;
             }
             commit<PAIR>(&empty[slot]);
@@ -890,12 +920,19 @@ int launch_a16w4_tc(const A16W4Call& call, bool grad, void* ws, cudaStream_t st)
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return QG_ERR_CUDA;
   }
-  {
-    cuuint64_t dims[2] = {(cuuint64_t)a.R, (cuuint64_t)c.in_rows};
-    cuuint64_t strides[1] = {(cuuint64_t)c.ld_in * 2};
-    cuuint32_t box[2] = {KS, XBOX};
-    cuuint32_t es[2] = {1, 1};
-    if (g_tc_encode(&m.rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (void*)c.in, dims, strides, box, es,
+  // Rows as [64-wide block of the reduction][row][64], or plainly [row][R]
+  // where the last block is a partial one, which only this form ends in zeros.
+  a.whole = a.R % KS == 0;
+  for (int b = 0; b < kBoxes; ++b) {
+    const cuuint32_t rows = (cuuint32_t)box_rows(b);
+    cuuint64_t dims3[3] = {KS, (cuuint64_t)c.in_rows, (cuuint64_t)a.subs};
+    cuuint64_t strides3[2] = {(cuuint64_t)c.ld_in * 2, KS * 2};
+    cuuint32_t box3[3] = {KS, rows, SUBS};
+    cuuint64_t dims2[2] = {(cuuint64_t)a.R, (cuuint64_t)c.in_rows};
+    cuuint32_t box2[2] = {KS, rows};
+    cuuint32_t es[3] = {1, 1, 1};
+    if (g_tc_encode(&m.rows[b], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.whole ? 3 : 2, (void*)c.in,
+                    a.whole ? dims3 : dims2, strides3, a.whole ? box3 : box2, es,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
