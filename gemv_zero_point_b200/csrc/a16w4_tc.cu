@@ -40,8 +40,9 @@
 //               groups of eight warps that take the stages in turn (one stage
 //               takes a group about 700 cycles, mostly latencies)
 // Indirect rows are first brought into sorted order in the workspace (about
-// 45 us for 32768 rows of 2048, next to 260): gathering them here took 963 us
-// in all with tensor-map row gathers of four rows, 534 with cp.async.
+// 45 us for 32768 rows of 2048, 215 us in all with 64 experts of 1536
+// features): gathering them here took 963 us in all with tensor-map row
+// gathers of four rows, 534 with cp.async.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -194,12 +195,14 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Every lane waits; the warp takes its decision together.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status) {
+// Every lane waits; the warp takes its decision together.  The limit counts
+// the pipeline's own time: a role waits for the work before this call first.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status,
+                                          uint32_t limit = kSpinLimit) {
   // a phase that is complete is seen at once; a parked wait costs about 180
   // cycles even then
   if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_park(bar, parity, status));
+  return __all_sync(0xffffffffu, mbar_park(bar, parity, status, limit));
 }
 
 // A group scale (and zero) as the expansion uses it.
@@ -483,6 +486,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
       }
       for (int s = 0; s < stages; ++s, ++it) {
+        if (it == NRING) asm volatile("griddepcontrol.wait;" ::: "memory");  // from here on a wait can block
         ok = warp_wait(&n_empty[slot], par, status);  // the first round passes
         if (!ok) break;
         if (elect_one()) {
@@ -505,6 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ring's size, two barriers a stage and polled waits it took 1050 cycles a
     // stage, twice the MMAs' own time.
     if (rank == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       uint32_t use = 0, slot = 0, par = 0;
       bool ok = true;
       for (int64_t t = first; t < total && ok; t += step, ++use) {
@@ -572,7 +577,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t step_b = GRAD ? (uint32_t)(KST * G * SB) : 4u * SB;  // scales: stage to stage
     uint32_t it = 0, slot = group, ns = group;
     uint32_t par = 1, npar = 0;  // parities of the waits for a free slot and for nibbles
-    bool ok = true;
+    bool ok = true, early = true;
     for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
       const uint8_t* scl = c.packed + (int64_t)tl.e * c.expert_bytes + (int64_t)c.N * (c.K >> 1);
@@ -609,6 +614,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         now = next;
         next = fetch(s + 4);
+        if (early && par == 0) {  // from here on a wait can block
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          early = false;
+        }
         ok = warp_wait(&empty[slot], par, status);  // the first round passes
         if (!ok) break;
         const uint32_t dst = w_at + slot * (SUBS * W_BYTES);
@@ -649,7 +658,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int64_t t = first; t < total; t += step, ++use) {
       const Tile tl = tile_at(t);
       const uint32_t buf = use & 1;
-      if (!warp_wait(&t_full[buf], (use >> 1) & 1, status)) break;
+      // a whole reduction, of 2^24 at most
+      if (!warp_wait(&t_full[buf], (use >> 1) & 1, status, kSpinLimit << 4)) break;
       tc_fence_after();
       const int f = tl.f0 + 32 * q + lane;
       float b = 0.0f;
