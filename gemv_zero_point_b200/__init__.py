@@ -475,14 +475,20 @@ def _rows(t, dtype, what):
     ld, one = st
     if one != 1 and k != 1:
         raise ValueError(f"{what}: expected a row-major view")
-    if n <= 1 and ld < k:  # the stride of a single row says nothing
-        ld = k
+    if n <= 1:  # the stride of a single row says nothing
+        ld = (k + 7) & ~7
     return n, k, ld
 
 
 def _check_dense(t, dtype, shape, what):
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: expected contiguous {dtype} {shape}")
+
+
+def _workspace_size(t):
+    if not t.is_contiguous():
+        raise ValueError("workspace: expected contiguous memory")
+    return t.numel() * t.element_size()
 
 
 def _pos_topk(pos, T):
@@ -552,7 +558,7 @@ def qgemm_a16w4_bf16_experts(x, offsets, packed_w, y, src=None, topk=1, bias=Non
         _check_dense(bias, torch.float32, (E, N), "bias")
     have = 0
     if workspace is not None:
-        have = workspace.numel() * workspace.element_size()
+        have = _workspace_size(workspace)
     elif src is not None:
         have = lib.qgemm_a16w4_bf16_experts_workspace_bytes(E, S, K, 1)
         if have:
@@ -612,7 +618,7 @@ def qg_sort_by_expert(ids, offsets, src, pos, workspace=None, stream=None):
         if have:
             workspace = _empty_bytes(have, ids.device)
     else:
-        have = workspace.numel() * workspace.element_size()
+        have = _workspace_size(workspace)
     _launch(lib.qg_sort_by_expert, stream, ids.get_device(), (offsets, src, pos, workspace),
             (T, topk, E, ids.data_ptr(), ld, offsets.data_ptr(), src.data_ptr(), pos.data_ptr(),
              _addr(workspace), have))

@@ -689,7 +689,8 @@ int64_t packed_bytes(int N, int K, int format) {
 // Few rows per expert stream the weights past warp MMAs, more go to the
 // tensor cores.  One matrix: 16 rows at N = 14336, K = 4096 take 19 us here
 // and 23 there, 32 rows 34 and 24.  Experts (64 of 2048 x 2048): 4 rows each
-// take 62 us both ways, 16 rows 122 and 85.
+// take 62 us both ways, 16 rows 122 and 85.  The host knows the average
+// alone; an expert with more rows than it is right either way.
 bool few_rows(int E, int S) { return cdiv(S, E) <= (E > 1 ? 4 : 16); }
 
 // Checks of every product: QG_OK when the call can run (S may be 0).
@@ -700,7 +701,8 @@ int product_args(int E, int S, int N, int K, const void* in, int64_t ld_in, int 
     return QG_ERR_INVALID_ARG;
   if (format != QG_W4_F32 && format != QG_W4_BF16 && format != QG_W4_ASYM)
     return QG_ERR_INVALID_ARG;
-  if (K % 64 || E > kA16W4MaxExperts) return QG_ERR_UNSUPPORTED;
+  if (K % 64 || E > kA16W4MaxExperts || N > kA16W4MaxSide || K > kA16W4MaxSide)
+    return QG_ERR_UNSUPPORTED;
   if (S == 0) return QG_OK;
   if (!in || !packed || !out) return QG_ERR_INVALID_ARG;
   if (((uintptr_t)packed & 15) || ((uintptr_t)in & 15) || ld_in % 8 || ((uintptr_t)out & 1) ||

@@ -27,6 +27,7 @@ struct A16W4Call {
   int64_t ld_out;
 };
 constexpr int kA16W4MaxExperts = 1024;
+constexpr int kA16W4MaxSide = 1 << 24;  // N and K, either of which is a reduction
 int launch_a16w4_rows(const A16W4Call& c, cudaStream_t st);           // few rows (a16w4.cu)
 // many rows (a16w4_tc.cu); indirect rows need a workspace to be sorted in
 int launch_a16w4_tc(const A16W4Call& c, bool grad, void* ws, cudaStream_t st);
@@ -84,11 +85,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+constexpr uintptr_t kMaxPrefetch = 1u << 26;  // more would only displace itself
 // L2 prefetch of the 16-byte-aligned interior of [p, p + bytes).
 __device__ __forceinline__ void prefetch_l2(const void* p, int64_t bytes) {
   const uintptr_t b = ((uintptr_t)p + 15) & ~(uintptr_t)15;
   const uintptr_t e = ((uintptr_t)p + (uintptr_t)bytes) & ~(uintptr_t)15;
-  if (e > b) bulk_prefetch_l2((const void*)b, (uint32_t)(e - b));
+  if (e > b) bulk_prefetch_l2((const void*)b, (uint32_t)(e - b < kMaxPrefetch ? e - b : kMaxPrefetch));
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -102,29 +104,11 @@ __device__ __forceinline__ uint32_t bf16x2_minus136(uint32_t v) {
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x43084308u));
   return d;
 }
-// Named barriers with an AND over a predicate, so every thread of a role
-// takes the same decision after a bounded wait.
-template <int ID, int N>
-__device__ __forceinline__ bool bar_and(bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)v), "n"(ID), "n"(N)
-      : "memory");
-  return r != 0;
-}
-template <int ID, int N>
-__device__ __forceinline__ void bar_sync() {
-  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
-}
-
 // Wait for phase `parity` of `bar` with mbarrier.try_wait and a suspend-time
 // hint: the hardware parks the thread until the phase completes (or the
 // 20 us hint runs out, after which it asks again), so a waiting warp takes no
-// issue slots from the converter warps on its sub-partition.  At most limit / 256 + 1 tries: about 82 ms at kSpinLimit,
-// 0.3 ms at kStallSpinLimit.
+// issue slots from the other warps on its sub-partition.  At most
+// limit / 256 + 1 tries: about 82 ms at kSpinLimit.
 __device__ __forceinline__ bool mbar_park(uint64_t* bar, uint32_t parity, int* status,
                                           uint32_t limit = kSpinLimit) {
   const uint32_t tries = (limit >> 8) + 1;

@@ -422,11 +422,17 @@ int qconv2d_f32_dyn_a8w4(int Nb, int H, int W, int Cin, int Cout, int KH, int KW
  *   x: bf16 [M][ldx] (ldx >= K), 16-byte aligned, ldx % 8 == 0
  *   packed_w: 16-byte aligned, in the packing that `format` names (qg_w4_format)
  *   bias: f32 [N] or NULL;  y: bf16 [M][ldy] (ldy >= N), any alignment
- * K % 64 == 0 (else QG_ERR_UNSUPPORTED); M >= 0, any N >= 1.  No workspace.
- * Sums are held in f32 and y is rounded once.  A few rows use the exact int4
- * codes; for many rows each weight w[n,k] is rounded to bf16 first (half a
- * step, 2^-8 of it).  Rows of x do not mix: a non-finite value in one row
- * reaches that row of y alone.
+ * K % 64 == 0, N and K <= 16777216 (else QG_ERR_UNSUPPORTED); M >= 0, any
+ * N >= 1.  No workspace.
+ * Sums are held in f32 and y is rounded once.
+ *   Many rows: each weight w[n,k] is rounded to bf16 first (half a step,
+ *   2^-8 of it).
+ *   A few rows (up to 16, up to 4 per expert on average): the codes are used
+ *   exactly, as c + 136 in sums that start at -136 * sum_k x over the group.
+ *   That costs the group's f32 sum about 5 of its 24 bits, and a group whose
+ *   sum |x| reaches 2^120 overflows.
+ * Rows of x do not mix: a non-finite value in one row reaches that row of y
+ * alone, which is then NaN or infinite there.
  * ------------------------------------------------------------------------ */
 typedef enum {
   QG_W4_F32 = 0,  /* pack_w4_g32: f32 group scales */
@@ -447,11 +453,13 @@ int qgemm_a16w4_bf16(int M, int N, int K, const void* x, int64_t ldx, const void
  *   the pack's size, a multiple of 16);  bias: f32 [E][N] or NULL
  *   y: bf16 [S][ldy].  Rows that belong to no expert (before offsets[0],
  *   from offsets[E] on) are left as they are.
- * E <= 1024, K % 64 == 0 (else QG_ERR_UNSUPPORTED).  Nothing is read back to
- * the host.  Workspace: qgemm_a16w4_bf16_experts_workspace_bytes(E, S, K,
- * src != NULL), 256-byte aligned (0: none; with src and many rows per expert
- * the rows are first brought into sorted order there).  An expert whose range is not inside [0, S) gets no rows, and a
- * src entry that reaches outside x counts as a row of zeros; both record
+ * E <= 1024, K % 64 == 0, N and K <= 16777216 (else QG_ERR_UNSUPPORTED).
+ * Nothing is read back to the host.  Workspace:
+ * qgemm_a16w4_bf16_experts_workspace_bytes(E, S, K, src != NULL), 256-byte
+ * aligned (0: none; with src and many rows per expert the rows are first
+ * brought into sorted order there).
+ * An expert whose range is not inside [0, S] gets no rows, and a src entry
+ * that reaches outside x counts as a row of zeros; both record
  * QG_ERR_INVALID_ARG in the device status.
  */
 size_t qgemm_a16w4_bf16_experts_workspace_bytes(int E, int S, int K, int indirect);
