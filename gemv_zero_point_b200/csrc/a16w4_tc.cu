@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     prefetch_tmap(&maps.nib);
     for (int b = 0; b < kBoxes; ++b) prefetch_tmap(&maps.rows[b]);
   }
+  __syncwarp();
   if (warp == 1) {
     if constexpr (PAIR) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (lane == 0) pre[c.E] = carry;
   }
+  __syncwarp();
   tc_fence_before();
   // in a pair, both CTAs' barriers exist before any signal between them
   if constexpr (PAIR) cluster_sync_all(); else __syncthreads();
@@ -457,11 +459,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-    // every copy has landed before the CTA may exit (in a pair the first CTA
-    // waits for both, and the CTAs end together)
-    if (rank == 0)
-      for (uint32_t k = it > STAGES ? it - STAGES : 0; k < it; ++k)
-        warp_wait(&full[k % STAGES], (k / STAGES) & 1, status);
+    // Every copy has landed (in a pair the first CTA waits for both, and the
+    // CTAs end together) and every commit has arrived before the CTA may exit.
+    for (uint32_t k = it > STAGES ? it - STAGES : 0; k < it; ++k) {
+      if (rank == 0) warp_wait(&full[k % STAGES], (k / STAGES) & 1, status);
+      if (ok) warp_wait(&empty[k % STAGES], (k / STAGES) & 1, status);
+    }
   } else if (warp == 2) {
     // ---------------- nibbles (inputs of the call alone) ----------------
     uint32_t it = 0, slot = 0, par = 1;
@@ -552,7 +555,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      if (!ok) {  // MMAs in flight end before their operands or TMEM go away
+      if (ok) {  // the epilogues' last signals have arrived, the other CTA's among them
+        for (uint32_t k = use > 2 ? use - 2 : 0; k < use; ++k)
+          warp_wait(&t_empty[k & 1], (k >> 1) & 1, status);
+      } else {  // MMAs in flight end before their operands or TMEM go away
         if (elect_one()) commit<PAIR>(drain);
         __syncwarp();
         warp_wait(drain, 0, status);
@@ -666,6 +672,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (c.bias && f < a.F) b = __ldg(c.bias + (int64_t)tl.e * a.F + f);
       for (int j0 = 0; j0 < tl.np; j0 += 32) {
         uint32_t v[32];
+        __syncwarp();  // converged again after the stores, as the load asks
         tmem_ld32(tmem_base + ((uint32_t)(32 * q) << 16) + buf * TT + j0, v);
         tmem_wait_ld();
         if constexpr (SHARED) {
