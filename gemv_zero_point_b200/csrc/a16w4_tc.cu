@@ -68,9 +68,19 @@ __host__ __device__ constexpr int box_rows(int i) { return 32 << i; }
 __device__ __forceinline__ int box_of(int rows) { return rows <= 32 ? 0 : rows <= 64 ? 1 : 2; }
 constexpr int STAGES = 3;
 constexpr int NRING = 3;
+// Signals that the two expansion groups wait for have a barrier per stage mod
+// 6, not per slot: a group sees every other stage, so with three barriers it
+// would see every other phase of each, and a wait by parity passes when the
+// phase before the skipped one is the last to have ended (the copies of two
+// slots may land out of order).  With six, every phase of a barrier is waited
+// for by the one group that uses it.
+constexpr int NBAR = 6;
+static_assert(STAGES == 3 && NRING == 3, "stages mod 6 give the slot and the group");
+constexpr int kBarriers = STAGES + 2 * NBAR + NRING + 5;
 constexpr int X_BYTES = XR * KS * 2;       // 16 KiB per sub-tile
 constexpr int W_BYTES = TF * KS * 2;       // 16 KiB per sub-tile
 constexpr int NIB_BYTES = TF * KST / 2;    // 8 KiB per stage
+static_assert(kBarriers + 1 + kBoxes <= 32, "one warp sets them up");
 constexpr int kFewRows = 64;               // rows of a tile up to which its weights' bytes count
 constexpr int THREADS = 768;
 constexpr int EPI_WARP0 = 4, CONV_WARP0 = 8, CONV_WARPS = 8;  // CONV_WARPS per group
@@ -318,9 +328,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t sX = smem_u32(smem), sW = smem_u32(smem + OFF_W);
   const uint32_t sN = smem_u32(smem + OFF_N);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // rows and weights of a stage
-  uint64_t* empty = full + STAGES;
-  uint64_t* n_full = empty + STAGES;
-  uint64_t* n_empty = n_full + NRING;
+  uint64_t* empty = full + STAGES;  // [NBAR] by stage: its MMAs have ended
+  uint64_t* n_full = empty + NBAR;  // [NBAR] by stage
+  uint64_t* n_empty = n_full + NBAR;
   uint64_t* t_full = n_empty + NRING;
   uint64_t* t_empty = t_full + 2;
   uint64_t* drain = t_empty + 2;
@@ -336,23 +346,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1 + (PAIR ? 2 * CONV_WARPS : CONV_WARPS));
-      mbar_init(&empty[s], 1);
+  if (warp == 0) {  // a barrier per lane
+    constexpr uint32_t kConv = PAIR ? 2 * CONV_WARPS : CONV_WARPS;
+    if (lane < kBarriers) {
+      uint64_t* bar = full + lane;
+      mbar_init(bar, bar < empty ? 1 + kConv : bar < n_empty ? 1 : bar < t_full ? CONV_WARPS
+                     : bar < t_empty ? 1 : bar < drain ? (PAIR ? 8 : 4) : 1);
+    } else if (lane - kBarriers < 1 + kBoxes) {
+      prefetch_tmap(lane == kBarriers ? &maps.nib : &maps.rows[lane - kBarriers - 1]);
     }
-    for (int s = 0; s < NRING; ++s) {
-      mbar_init(&n_full[s], 1);
-      mbar_init(&n_empty[s], CONV_WARPS);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&t_full[b], 1);
-      mbar_init(&t_empty[b], PAIR ? 8 : 4);
-    }
-    mbar_init(drain, 1);
     fence_mbar_init();
-    prefetch_tmap(&maps.nib);
-    for (int b = 0; b < kBoxes; ++b) prefetch_tmap(&maps.rows[b]);
   }
   __syncwarp();
   if (warp == 1) {
@@ -427,7 +430,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0) {
     // ---------------- rows: this CTA's half, or all ----------------
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    uint32_t it = 0, slot = 0, par = 1;
+    // `free`: the barrier of the stage that had the slot before
+    uint32_t it = 0, slot = 0, free = NBAR - STAGES, par = 1;
     bool ok = true;
     for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t sub_b = (uint32_t)box_rows(box) * (KS * 2);  // bytes of a sub-tile
       const void* map = &maps.rows[box];
       for (int s = 0; s < stages; ++s, ++it) {
-        ok = warp_wait(&empty[slot], par, status);  // the first round passes
+        ok = warp_wait(&empty[free], par, status);  // the first round passes
         if (!ok) break;
         const int subs = a.whole ? SUBS : min(SUBS, a.subs - SUBS * (s_first + s));
         if (elect_one()) {
@@ -453,8 +457,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         __syncwarp();
-        if (++slot == STAGES) {
-          slot = 0;
+        if (++slot == STAGES) slot = 0;
+        if (++free == NBAR) {
+          free = 0;
           par ^= 1;
         }
       }
@@ -463,11 +468,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     // CTAs end together) and every commit has arrived before the CTA may exit.
     for (uint32_t k = it > STAGES ? it - STAGES : 0; k < it; ++k) {
       if (rank == 0) warp_wait(&full[k % STAGES], (k / STAGES) & 1, status);
-      if (ok) warp_wait(&empty[k % STAGES], (k / STAGES) & 1, status);
+      if (ok) warp_wait(&empty[k % NBAR], (k / NBAR) & 1, status);
     }
   } else if (warp == 2) {
     // ---------------- nibbles (inputs of the call alone) ----------------
-    uint32_t it = 0, slot = 0, par = 1;
+    uint32_t it = 0, slot = 0, bar = 0, par = 1;
     bool ok = true;
     for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
@@ -493,11 +498,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = warp_wait(&n_empty[slot], par, status);  // the first round passes
         if (!ok) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&n_full[slot], NIB_BYTES);
-          if (GRAD) tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, tl.f0 / 8, (s_first + s) * KST, tl.e, &n_full[slot]);
-          else tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, (s_first + s) * (KST / 8), tl.f0, tl.e, &n_full[slot]);
+          mbar_arrive_expect_tx(&n_full[bar], NIB_BYTES);
+          if (GRAD) tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, tl.f0 / 8, (s_first + s) * KST, tl.e, &n_full[bar]);
+          else tma_load_3d(sN + slot * NIB_BYTES, &maps.nib, (s_first + s) * (KST / 8), tl.f0, tl.e, &n_full[bar]);
         }
         __syncwarp();
+        if (++bar == NBAR) bar = 0;
         if (++slot == NRING) {
           slot = 0;
           par ^= 1;
@@ -505,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     for (uint32_t k = it > NRING ? it - NRING : 0; k < it; ++k)
-      warp_wait(&n_full[k % NRING], (k / NRING) & 1, status);
+      warp_wait(&n_full[k % NBAR], (k / NBAR) & 1, status);
   } else if (warp == 1) {
     // ---------------- MMA issue ----------------
     // One thread, and every stage passes through it: with divisions by the
@@ -513,7 +519,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // stage, twice the MMAs' own time.
     if (rank == 0) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      uint32_t use = 0, slot = 0, par = 0;
+      uint32_t use = 0, slot = 0, bar = 0, par = 0;
       bool ok = true;
       for (int64_t t = first; t < total && ok; t += step, ++use) {
         const Tile tl = tile_at(t);
@@ -545,10 +551,11 @@ __global__ void __launch_bounds__(THREADS, 1)
               dx += next_x;
               dw += W_BYTES >> 4;
             }
-            commit<PAIR>(&empty[slot]);
+            commit<PAIR>(&empty[bar]);
             if (s == stages - 1) commit<PAIR>(&t_full[buf]);
           }
           __syncwarp();
+          if (++bar == NBAR) bar = 0;
           if (++slot == STAGES) {
             slot = 0;
             par ^= 1;
@@ -581,8 +588,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                                      : half * W_BYTES + row * 128);
     const uint32_t turn = (uint32_t)((row & 7) ^ (half << 2));  // swizzle, and the groups' order
     const uint32_t step_b = GRAD ? (uint32_t)(KST * G * SB) : 4u * SB;  // scales: stage to stage
-    uint32_t it = 0, slot = group, ns = group;
-    uint32_t par = 1, npar = 0;  // parities of the waits for a free slot and for nibbles
+    uint32_t it = 0, slot = group;                 // of the stage and of its nibbles
+    uint32_t nib = group, free = group + NBAR - STAGES;  // barriers
+    uint32_t npar = 0, par = 1;                    // and the parities to wait for
     bool ok = true, early = true;
     for (int64_t t = first; t < total && ok; t += step) {
       const Tile tl = tile_at(t);
@@ -598,16 +606,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       int s = (it & 1) == group ? 0 : 1;  // this group's stages: every other one
       RawScales now = fetch(s), next = fetch(s + 2);
       for (; s < stages; s += 2) {
-        ok = warp_wait(&n_full[ns], npar, status);
+        ok = warp_wait(&n_full[nib], npar, status);
         if (!ok) break;
         uint32_t wd[8];
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(wd[0]), "=r"(wd[1]), "=r"(wd[2]), "=r"(wd[3])
-                     : "r"(sN + ns * NIB_BYTES + nib_at)
+                     : "r"(sN + slot * NIB_BYTES + nib_at)
                      : "memory");
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(wd[4]), "=r"(wd[5]), "=r"(wd[6]), "=r"(wd[7])
-                     : "r"(sN + ns * NIB_BYTES + nib_at + 16)
+                     : "r"(sN + slot * NIB_BYTES + nib_at + 16)
                      : "memory");
         // the halves' 16-byte parts lie in the same banks: the second half
         // stores its second group first
@@ -624,7 +632,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           asm volatile("griddepcontrol.wait;" ::: "memory");
           early = false;
         }
-        ok = warp_wait(&empty[slot], par, status);  // the first round passes
+        ok = warp_wait(&empty[free], par, status);  // the first round passes
         if (!ok) break;
         const uint32_t dst = w_at + slot * (SUBS * W_BYTES);
 #pragma unroll
@@ -638,17 +646,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&n_empty[ns]);
+          mbar_arrive(&n_empty[slot]);
           if constexpr (PAIR) mbar_arrive_cluster(mapa(smem_u32(&full[slot]), 0));
           else mbar_arrive(&full[slot]);
         }
-        if ((slot += 2) >= STAGES) {
-          slot -= STAGES;
-          par ^= 1;
-        }
-        if ((ns += 2) >= NRING) {
-          ns -= NRING;
+        if ((slot += 2) >= STAGES) slot -= STAGES;
+        if ((nib += 2) >= NBAR) {
+          nib -= NBAR;
           npar ^= 1;
+        }
+        if ((free += 2) >= NBAR) {
+          free -= NBAR;
+          par ^= 1;
         }
       }
       it += (uint32_t)stages;

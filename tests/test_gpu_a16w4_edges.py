@@ -270,3 +270,36 @@ def test_behind_long_work(lib):
     assert torch.equal(dx2.view(torch.int16), dx.view(torch.int16))
     # f32 sums of ones: exact up to 2^24 per thread, and powers of two after it
     assert torch.equal(dw, torch.full_like(dw, float(N)))
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_cold_memory(lib, grad):
+    """Weights in memory that no kernel has read yet, where tensor copies land
+    out of order: the bits of later calls."""
+    rng = np.random.default_rng(3)
+    E, N, K, S = 64, 1728, 2496, 6000
+    cut = np.sort(rng.integers(0, S + 1, E - 1))
+    off = torch.tensor([0, *cut.tolist(), S], dtype=torch.int32, device="cuda")
+    want = None
+    for k in range(6):
+        torch.cuda.empty_cache()
+        g = torch.Generator(device="cuda").manual_seed(1)
+        packed = torch.randint(0, 256, (E, N * K // 2 + N * K // 16), generator=g, device="cuda",
+                               dtype=torch.uint8)
+        scales = packed[:, N * K // 2:]
+        scales.copy_(torch.full((E, N * K // 32), 0.01, dtype=BF, device="cuda").view(torch.uint8))
+        rows = torch.randn((S, N if grad else K), generator=g, device="cuda").to(BF)
+        out = torch.empty((S, K if grad else N), dtype=BF, device="cuda")
+        fresh = torch.empty_like(packed)  # its pages are first touched by the copy engine's writes
+        torch.cuda.synchronize()
+        fresh.copy_(packed)
+        call = lib.qgemm_a16w4_bf16_experts_grad_x if grad else lib.qgemm_a16w4_bf16_experts
+        call(rows, off, fresh, out, weights="bf16")
+        if want is None:
+            again = torch.empty_like(out)
+            call(rows, off, fresh, again, weights="bf16")
+            want = again.cpu().view(torch.int16)
+            del again
+        assert torch.equal(out.cpu().view(torch.int16), want), k
+        assert lib.qg_device_status(True) == 0
+        del packed, scales, rows, out, fresh
