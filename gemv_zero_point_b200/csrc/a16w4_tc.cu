@@ -617,6 +617,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                      : "=r"(wd[4]), "=r"(wd[5]), "=r"(wd[6]), "=r"(wd[7])
                      : "r"(sN + slot * NIB_BYTES + nib_at + 16)
                      : "memory");
+        // Once they are in registers the next copy into the slot may leave.
+        // The signal depends on the values themselves: behind the loads in
+        // program order alone it went ahead of them.
+        const uint32_t seen = (wd[0] | wd[1] | wd[2]) | (wd[3] | wd[4] | wd[5]) | (wd[6] | wd[7]);
+        const int signaller = __any_sync(0xffffffffu, seen != 0) ? 0 : 1;
+        if (lane == signaller) mbar_arrive(&n_empty[slot]);
         // the halves' 16-byte parts lie in the same banks: the second half
         // stores its second group first
         const Scale<FMT> sc[2] = {make_scale<FMT>(now, half), make_scale<FMT>(now, half ^ 1)};
@@ -646,7 +652,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&n_empty[slot]);
           if constexpr (PAIR) mbar_arrive_cluster(mapa(smem_u32(&full[slot]), 0));
           else mbar_arrive(&full[slot]);
         }
