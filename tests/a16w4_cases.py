@@ -14,7 +14,14 @@ Tolerance of one output y = sum_k x[k] w[k] + b, stored as bf16:
     independent of one another, so by Hoeffding's inequality their sum passes
     6.5 * 2^-8 * Q, Q = sqrt(sum_k (x w)^2), with a probability below 2e-9
     per output.  The sum of a weight's scale and zero parts is formed before
-    that rounding.
+    that rounding;
+  - where it multiplies codes (few rows) as c + 136 in sums that start at
+    -136 X: the values of a group's sum stay below 280 sw sum |x|, and its 34
+    additions are off by 2^-23 of that each, at most 0.0011 sw sum |x| in all.
+    Over independent groups Hoeffding's 6.5 sigma is then, for |x| of one size,
+    6.5 * 0.0011 * 32 * sqrt(K/32) sw |x| = 0.23 sqrt(K/32) sw |x|.  With codes
+    spread evenly over [-8, 7], as here, the bf16 term above is
+    6.5 * 2^-8 * 4.6 * sqrt(K) sw |x| = 0.66 sqrt(K/32) sw |x|: it stands for both.
 """
 import numpy as np
 
