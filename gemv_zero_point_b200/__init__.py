@@ -432,13 +432,20 @@ def qconv2d_f32_dyn_a8w4(x, packed_w, Cout, KH, KW, stride, pad, bias, clamp_min
 W4_FORMATS = {"f32": 0, "bf16": 1, "asym": 2}  # qg_w4_format
 _W4_GROUP_BYTES = (4, 2, 8)
 _DTYPES = {}                                   # torch dtype -> qg_dtype
+_torch_module = _raw_stream = _current_device = None
 
 
 def _torch():
-    import torch
-    if not _DTYPES:
+    """torch, imported by the first call that needs it; an import statement in
+    every call, found loaded or not, costs more than this."""
+    global _torch_module, _raw_stream, _current_device
+    if _torch_module is None:
+        import torch
         _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    return torch
+        # current_stream(dev) and current_device() without building objects
+        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _torch_module = torch
+    return _torch_module
 
 
 def _launch(fn, stream, dev, others, args):
@@ -447,20 +454,16 @@ def _launch(fn, stream, dev, others, args):
     current one unless one is given.  One call from Python costs about as much
     as the smallest kernels here run, so this and the checks below touch each
     tensor as little as they can."""
-    torch = _torch()
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{fn.__name__}: the tensors are not on one device")
     if dev < 0:
         raise ValueError(f"{fn.__name__}: expected CUDA tensors")
-    if stream is not None:
-        stream = _stream(stream)
-    else:  # current_stream(dev) without building a Stream object
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch._C._cuda_getDevice() == dev:
+    stream = _raw_stream(dev) if stream is None else _stream(stream)
+    if _current_device() == dev:
         rc = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
+        with _torch_module.cuda.device(dev):
             rc = fn(*args, stream)
     if rc:
         raise QGError(rc, fn.__name__)
@@ -492,12 +495,11 @@ def _workspace_size(t):
 
 
 def _pos_topk(pos, T):
-    torch = _torch()
-    if pos.dim() != 2:
-        raise ValueError("pos: expected [T][topk]")
-    topk = pos.shape[1]
-    _check_dense(pos, torch.int32, (T, topk), "pos")
-    return topk
+    shape = pos.shape
+    if len(shape) != 2 or shape[0] != T or pos.dtype is not _torch_module.int32 or \
+            not pos.is_contiguous():
+        raise ValueError(f"pos: expected contiguous int32 [{T}][topk]")
+    return shape[1]
 
 
 def _addr(t):
@@ -625,7 +627,8 @@ def qg_sort_by_expert(ids, offsets, src, pos, workspace=None, stream=None):
 
 
 def _row_type(t):
-    _torch()
+    if _torch_module is None:
+        _torch()
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise ValueError("the rows are float32, bfloat16 or float16")
