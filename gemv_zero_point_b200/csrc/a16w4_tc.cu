@@ -44,7 +44,7 @@
 //               groups of eight warps that take the stages in turn (one stage
 //               takes a group about 700 cycles, mostly latencies)
 // Indirect rows are first brought into sorted order in the workspace (about
-// 45 us for 32768 rows of 2048, 215 us in all with 64 experts of 1536
+// 24 us for 32768 rows of 2048, 215 us in all with 64 experts of 1536
 // features): gathering them here took 963 us in all with tensor-map row
 // gathers of four rows, 534 with cp.async.
 #include <cuda.h>
