@@ -211,9 +211,10 @@ struct Pack : Words<T, V> {};
 template <typename T>
 struct Pack<T, 1> : Words<T, 1, T, 1> {};  // a value on its own
 
-__device__ __forceinline__ void unpack(const Words<float, 4>& p, float (&f)[4]) {
+template <int V>
+__device__ __forceinline__ void unpack(const Words<float, V>& p, float (&f)[V]) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(p.w[k]);
+  for (int k = 0; k < V; ++k) f[k] = __uint_as_float(p.w[k]);
 }
 template <int V>
 __device__ __forceinline__ void unpack(const Words<__nv_bfloat16, V>& p, float (&f)[V]) {
@@ -240,9 +241,10 @@ __device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, 1>& p, float (&
   f[0] = __bfloat162float(p.w[0]);
 }
 
-__device__ __forceinline__ void pack(const float (&f)[4], Words<float, 4>& p) {
+template <int V>
+__device__ __forceinline__ void pack(const float (&f)[V], Words<float, V>& p) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) p.w[k] = __float_as_uint(f[k]);
+  for (int k = 0; k < V; ++k) p.w[k] = __float_as_uint(f[k]);
 }
 template <int V>
 __device__ __forceinline__ void pack(const float (&f)[V], Words<__nv_bfloat16, V>& p) {
@@ -281,33 +283,39 @@ __device__ __forceinline__ int place_of(const int32_t* pos, int64_t i, int64_t S
 
 constexpr int JB = 8;  // experts of a token taken together
 
-template <typename W>
-__global__ void __launch_bounds__(256)
-    spread_rows_kernel(int topk, int64_t S, int64_t nv, const W* __restrict__ x,
-                                   int64_t ldx, const int32_t* __restrict__ pos,
-                                   W* __restrict__ xs, int64_t ldxs, int* status) {
+// Accesses of `bytes` that a thread has in flight per row: narrow ones (rows
+// whose start or length is no multiple of 16 bytes) come in several, so that
+// about as much is on its way as with 16-byte ones.
+constexpr int in_flight(int bytes) { return bytes >= 16 ? 1 : bytes == 8 ? 2 : 4; }
+
+template <typename W, int U>
+__global__ void __launch_bounds__(256, 4)
+    spread_rows_kernel(int topk, int64_t S, int64_t nv, const W* __restrict__ x, int64_t ldx,
+                       const int32_t* __restrict__ pos, W* __restrict__ xs, int64_t ldxs,
+                       int* status) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t t = blockIdx.x;
   const W* xr = x + t * ldx;
-  const int64_t i0 = (int64_t)blockIdx.y * blockDim.x * 2 + threadIdx.x;
-  const int64_t step = (int64_t)gridDim.y * blockDim.x * 2;
+  const int64_t i0 = (int64_t)blockIdx.y * blockDim.x * U + threadIdx.x;
+  const int64_t step = (int64_t)gridDim.y * blockDim.x * U;
   for (int jb = 0; jb < topk; jb += JB) {
     int64_t p[JB];
 #pragma unroll
     for (int j = 0; j < JB; ++j)
       p[j] = jb + j < topk ? place_of(pos, t * topk + jb + j, S, status) : -1;
     for (int64_t i = i0; i < nv; i += step) {
-      const int64_t i2 = i + blockDim.x;
-      const W a = xr[i];
-      W b = a;
-      if (i2 < nv) b = xr[i2];
+      W a[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u * (int)blockDim.x < nv) a[u] = xr[i + u * (int)blockDim.x];
 #pragma unroll
       for (int j = 0; j < JB; ++j) {
         if (p[j] < 0) continue;
         W* d = xs + p[j] * ldxs;
-        d[i] = a;
-        if (i2 < nv) d[i2] = b;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i + u * (int)blockDim.x < nv) d[i + u * (int)blockDim.x] = a[u];
       }
     }
   }
@@ -316,8 +324,8 @@ __global__ void __launch_bounds__(256)
 // Positions (and weights) first, then the loads of all JB rows, then the sums:
 // a row's load between two checks of positions waited for the one before it
 // (8192 tokens x 8 rows of 4096 bf16: 282 us).
-template <typename T, int V>
-__global__ void __launch_bounds__(256, 3)
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(256, U == 1 ? 3 : 2)
     combine_rows_kernel(int topk, int64_t S, int64_t nv, const T* __restrict__ ys, int64_t ldys,
                         const int32_t* __restrict__ pos, const float* __restrict__ w,
                         T* __restrict__ y, int64_t ldy, int* status) {
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(256, 3)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t t = blockIdx.x;
-  const int64_t step = (int64_t)gridDim.y * blockDim.x;
+  const int64_t step = (int64_t)gridDim.y * blockDim.x * U;
   int p[JB];
   float wj[JB];
   auto places = [&](int jb) {
@@ -336,34 +344,48 @@ __global__ void __launch_bounds__(256, 3)
     }
   };
   if (topk <= JB) places(0);
-  for (int64_t i = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; i < nv; i += step) {
-    float acc[V];
+  for (int64_t i = (int64_t)blockIdx.y * blockDim.x * U + threadIdx.x; i < nv; i += step) {
+    float acc[U][V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[u][k] = 0.0f;
     for (int jb = 0; jb < topk; jb += JB) {
       if (topk > JB) places(jb);
-      P r[JB];
-#pragma unroll
-      for (int j = 0; j < JB; ++j)
-        if (p[j] >= 0) r[j] = reinterpret_cast<const P*>(ys + (int64_t)p[j] * ldys)[i];
+      P r[JB][U];
 #pragma unroll
       for (int j = 0; j < JB; ++j) {
         if (p[j] < 0) continue;
-        float v[V];
-        unpack(r[j], v);
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = fmaf(wj[j], v[k], acc[k]);
+        for (int u = 0; u < U; ++u)
+          if (u == 0 || i + u * (int)blockDim.x < nv) 
+            r[j][u] = reinterpret_cast<const P*>(ys + (int64_t)p[j] * ldys)[i + u * (int)blockDim.x];
+      }
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        if (p[j] < 0) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float v[V];
+          unpack(r[j][u], v);
+#pragma unroll
+          for (int k = 0; k < V; ++k) acc[u][k] = fmaf(wj[j], v[k], acc[u][k]);
+        }
       }
     }
-    P out;
-    pack(acc, out);
-    reinterpret_cast<P*>(y + t * ldy)[i] = out;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      P out;
+      pack(acc[u], out);
+      if (u == 0 || i + u * (int)blockDim.x < nv)
+        reinterpret_cast<P*>(y + t * ldy)[i + u * (int)blockDim.x] = out;
+    }
   }
 }
 
 // One CTA per token: the dot products of its experts' rows with dy[t] need
 // the whole row, and dy is read once for JB of them.
-template <typename T, int V>
+template <typename T, int V, int U>
 __global__ void __launch_bounds__(512)
     combine_grad_kernel(int topk, int64_t S, int64_t nv, const T* __restrict__ dy,
                                     int64_t lddy, const T* __restrict__ ys, int64_t ldys,
@@ -385,31 +407,43 @@ __global__ void __launch_bounds__(512)
       wj[j] = (w && p[j] >= 0) ? __ldg(w + t * topk + jb + j) : 1.0f;
       dot[j] = 0.0f;
     }
-    for (int64_t i = threadIdx.x; i < nv; i += blockDim.x) {
-      const P g = reinterpret_cast<const P*>(dy + t * lddy)[i];
-      float gf[V];
-      unpack(g, gf);
-      P r[JB];
+    for (int64_t i = threadIdx.x; i < nv; i += blockDim.x * U) {
+      P g[U], r[JB][U];
+      const P* from = reinterpret_cast<const P*>(dy + t * lddy) + i;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u == 0 || i + u * (int)blockDim.x < nv) g[u] = from[u * (int)blockDim.x];
       if (dw) {
 #pragma unroll
-        for (int j = 0; j < JB; ++j)
-          if (p[j] >= 0) r[j] = reinterpret_cast<const P*>(ys + (int64_t)p[j] * ldys)[i];
+        for (int j = 0; j < JB; ++j) {
+          if (p[j] < 0) continue;
+          const P* row = reinterpret_cast<const P*>(ys + (int64_t)p[j] * ldys) + i;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (u == 0 || i + u * (int)blockDim.x < nv) r[j][u] = row[u * (int)blockDim.x];
+        }
       }
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
-        if (p[j] < 0) continue;
-        float v[V];
-        if (dw) {
-          unpack(r[j], v);
+      for (int u = 0; u < U; ++u) {
+        if (u > 0 && i + u * (int)blockDim.x >= nv) break;
+        float gf[V];
+        unpack(g[u], gf);
 #pragma unroll
-          for (int k = 0; k < V; ++k) dot[j] = fmaf(gf[k], v[k], dot[j]);
-        }
-        if (dys) {
-          P out;
+        for (int j = 0; j < JB; ++j) {
+          if (p[j] < 0) continue;
+          float v[V];
+          if (dw) {
+            unpack(r[j][u], v);
 #pragma unroll
-          for (int k = 0; k < V; ++k) v[k] = wj[j] * gf[k];
-          pack(v, out);
-          reinterpret_cast<P*>(dys + (int64_t)p[j] * lddys)[i] = out;
+            for (int k = 0; k < V; ++k) dot[j] = fmaf(gf[k], v[k], dot[j]);
+          }
+          if (dys) {
+            P out;
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = wj[j] * gf[k];
+            pack(v, out);
+            reinterpret_cast<P*>(dys + (int64_t)p[j] * lddys)[i + u * (int)blockDim.x] = out;
+          }
         }
       }
     }
@@ -466,17 +500,20 @@ template <typename T>
 int run_combine(int vec, int T_, int topk, int64_t S, int N, const void* ys, int64_t ldys,
                 const int32_t* pos, const float* w, void* y, int64_t ldy, cudaStream_t st) {
   const int64_t nv = N / vec;
-  const int th = row_threads(nv, 256);
+  const int u = in_flight(vec * (int)sizeof(T));
+  const int th = row_threads(cdiv(nv, u), 256);
   // a few tokens: several CTAs share a token's row
-  const int parts = (int)max64(1, min64(cdiv(nv, th), cdiv(2 * num_sms(), T_)));
+  const int parts = (int)max64(1, min64(cdiv(nv, th * u), cdiv(2 * num_sms(), T_)));
   const dim3 grid((unsigned)T_, (unsigned)parts);
   auto go = [&](auto kernel) {
     return launch_pdl(kernel, grid, th, 0, st, topk, S, nv, (const T*)ys, ldys, pos, w, (T*)y,
                       ldy, status_word());
   };
-  if (vec * sizeof(T) == 16) return go(combine_rows_kernel<T, 16 / sizeof(T)>);
-  if (vec * sizeof(T) == 4 && sizeof(T) == 2) return go(combine_rows_kernel<T, 4 / sizeof(T)>);
-  return go(combine_rows_kernel<T, 1>);
+  constexpr int B = (int)sizeof(T);
+  if (vec * B == 16) return go(combine_rows_kernel<T, 16 / B, in_flight(16)>);
+  if (vec * B == 8) return go(combine_rows_kernel<T, 8 / B, in_flight(8)>);
+  if (vec * B == 4) return go(combine_rows_kernel<T, 4 / B, in_flight(4)>);
+  return go(combine_rows_kernel<T, 1, in_flight(B)>);
 }
 
 template <typename T>
@@ -484,20 +521,22 @@ int run_combine_grad(int vec, int T_, int topk, int64_t S, int N, const void* dy
                      const void* ys, int64_t ldys, const int32_t* pos, const float* w, void* dys,
                      int64_t lddys, float* dw, cudaStream_t st) {
   const int64_t nv = N / vec;
-  const int th = row_threads(nv, T_ >= 8 * num_sms() ? 128 : 512);
+  const int th = row_threads(cdiv(nv, in_flight(vec * (int)sizeof(T))), T_ >= 8 * num_sms() ? 128 : 512);
   auto go = [&](auto kernel) {
     return launch_pdl(kernel, dim3((unsigned)T_), th, 0, st, topk, S, nv, (const T*)dy, lddy,
                       (const T*)ys, ldys, pos, w, (T*)dys, lddys, dw, status_word());
   };
-  if (vec * sizeof(T) == 16) return go(combine_grad_kernel<T, 16 / sizeof(T)>);
-  if (vec * sizeof(T) == 4 && sizeof(T) == 2) return go(combine_grad_kernel<T, 4 / sizeof(T)>);
-  return go(combine_grad_kernel<T, 1>);
+  constexpr int B = (int)sizeof(T);
+  if (vec * B == 16) return go(combine_grad_kernel<T, 16 / B, in_flight(16)>);
+  if (vec * B == 8) return go(combine_grad_kernel<T, 8 / B, in_flight(8)>);
+  if (vec * B == 4) return go(combine_grad_kernel<T, 4 / B, in_flight(4)>);
+  return go(combine_grad_kernel<T, 1, in_flight(B)>);
 }
 
 // Values per access that every pointer, stride and the row length allow.
 int vector_of(int esz, uintptr_t bits) {
-  if (all_aligned(bits, 16)) return 16 / esz;
-  if (esz == 2 && all_aligned(bits, 4)) return 2;
+  for (int b = 16; b > esz; b /= 2)
+    if (all_aligned(bits, b)) return b / esz;
   return 1;
 }
 
@@ -580,19 +619,21 @@ extern "C" int qg_spread_rows(int T, int topk, int S, int N, int dtype, const vo
   const int64_t rb = (int64_t)N * esz, xb = ldx * esz, sb = ldxs * esz;
   const uintptr_t bits = (uintptr_t)x | (uintptr_t)xs | (uintptr_t)rb | (uintptr_t)xb | (uintptr_t)sb;
   cudaStream_t st = (cudaStream_t)stream;
-  auto go = [&](auto kernel, auto* word) {
+  auto go = [&](auto* word) {
     using W = std::remove_pointer_t<decltype(word)>;
+    constexpr int U = sizeof(W) == 16 ? 2 : 4;
     const int64_t nv = rb / (int64_t)sizeof(W);
-    const int th = row_threads(cdiv(nv, 2), 256);
+    const int th = row_threads(cdiv(nv, U), 256);
     // a few tokens: several CTAs share a token's row
-    const int parts = (int)max64(1, min64(cdiv(nv, 2 * th), cdiv(2 * num_sms(), T)));
-    return launch_pdl(kernel, dim3((unsigned)T, (unsigned)parts), th, 0, st, topk, (int64_t)S, nv,
+    const int parts = (int)max64(1, min64(cdiv(nv, U * th), cdiv(2 * num_sms(), T)));
+    return launch_pdl(spread_rows_kernel<W, U>, dim3((unsigned)T, (unsigned)parts), th, 0, st, topk, (int64_t)S, nv,
                       (const W*)x, xb / (int64_t)sizeof(W), pos, (W*)xs, sb / (int64_t)sizeof(W),
                       status_word());
   };
-  if (all_aligned(bits, 16)) return go(spread_rows_kernel<uint4>, (uint4*)nullptr);
-  if (all_aligned(bits, 4)) return go(spread_rows_kernel<uint32_t>, (uint32_t*)nullptr);
-  return go(spread_rows_kernel<uint16_t>, (uint16_t*)nullptr);
+  if (all_aligned(bits, 16)) return go((uint4*)nullptr);
+  if (all_aligned(bits, 8)) return go((uint2*)nullptr);
+  if (all_aligned(bits, 4)) return go((uint32_t*)nullptr);
+  return go((uint16_t*)nullptr);
 }
 
 extern "C" int qg_combine_rows(int T, int topk, int S, int N, int dtype, const void* ys,
