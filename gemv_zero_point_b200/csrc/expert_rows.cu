@@ -19,6 +19,8 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "qg_internal.cuh"
 
 namespace qg {
@@ -281,14 +283,15 @@ __device__ __forceinline__ int place_of(const int32_t* pos, int64_t i, int64_t S
   return p < 0 ? -1 : p;
 }
 
-constexpr int JB = 8;  // experts of a token taken together
+// J experts of a token are taken together: 8, or 4 or 2 where topk is no more.
+// A thread has U accesses per row in flight: narrow ones (rows whose start or
+// length is no multiple of 16 bytes) come in several, and so do the rows of
+// few experts, so that about as much is on its way in every case.
+constexpr int in_flight(int bytes, int J) {
+  return (bytes >= 16 ? 1 : bytes == 8 ? 2 : 4) * (8 / J);
+}
 
-// Accesses of `bytes` that a thread has in flight per row: narrow ones (rows
-// whose start or length is no multiple of 16 bytes) come in several, so that
-// about as much is on its way as with 16-byte ones.
-constexpr int in_flight(int bytes) { return bytes >= 16 ? 1 : bytes == 8 ? 2 : 4; }
-
-template <typename W, int U>
+template <typename W, int U, int J>
 __global__ void __launch_bounds__(256, 4)
     spread_rows_kernel(int topk, int64_t S, int64_t nv, const W* __restrict__ x, int64_t ldx,
                        const int32_t* __restrict__ pos, W* __restrict__ xs, int64_t ldxs,
@@ -299,10 +302,10 @@ __global__ void __launch_bounds__(256, 4)
   const W* xr = x + t * ldx;
   const int64_t i0 = (int64_t)blockIdx.y * blockDim.x * U + threadIdx.x;
   const int64_t step = (int64_t)gridDim.y * blockDim.x * U;
-  for (int jb = 0; jb < topk; jb += JB) {
-    int64_t p[JB];
+  for (int jb = 0; jb < topk; jb += J) {
+    int64_t p[J];
 #pragma unroll
-    for (int j = 0; j < JB; ++j)
+    for (int j = 0; j < J; ++j)
       p[j] = jb + j < topk ? place_of(pos, t * topk + jb + j, S, status) : -1;
     for (int64_t i = i0; i < nv; i += step) {
       W a[U];
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(256, 4)
       for (int u = 0; u < U; ++u)
         if (i + u * (int)blockDim.x < nv) a[u] = xr[i + u * (int)blockDim.x];
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
+      for (int j = 0; j < J; ++j) {
         if (p[j] < 0) continue;
         W* d = xs + p[j] * ldxs;
 #pragma unroll
@@ -321,10 +324,10 @@ __global__ void __launch_bounds__(256, 4)
   }
 }
 
-// Positions (and weights) first, then the loads of all JB rows, then the sums:
+// Positions (and weights) first, then the loads of all J rows, then the sums:
 // a row's load between two checks of positions waited for the one before it
 // (8192 tokens x 8 rows of 4096 bf16: 282 us).
-template <typename T, int V, int U>
+template <typename T, int V, int U, int J>
 __global__ void __launch_bounds__(256, U == 1 ? 3 : 2)
     combine_rows_kernel(int topk, int64_t S, int64_t nv, const T* __restrict__ ys, int64_t ldys,
                         const int32_t* __restrict__ pos, const float* __restrict__ w,
@@ -334,27 +337,27 @@ __global__ void __launch_bounds__(256, U == 1 ? 3 : 2)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t t = blockIdx.x;
   const int64_t step = (int64_t)gridDim.y * blockDim.x * U;
-  int p[JB];
-  float wj[JB];
+  int p[J];
+  float wj[J];
   auto places = [&](int jb) {
 #pragma unroll
-    for (int j = 0; j < JB; ++j) {
+    for (int j = 0; j < J; ++j) {
       p[j] = jb + j < topk ? place_of(pos, t * topk + jb + j, S, status) : -1;
       wj[j] = w && p[j] >= 0 ? __ldg(w + t * topk + jb + j) : 1.0f;
     }
   };
-  if (topk <= JB) places(0);
+  if (topk <= J) places(0);
   for (int64_t i = (int64_t)blockIdx.y * blockDim.x * U + threadIdx.x; i < nv; i += step) {
     float acc[U][V];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int k = 0; k < V; ++k) acc[u][k] = 0.0f;
-    for (int jb = 0; jb < topk; jb += JB) {
-      if (topk > JB) places(jb);
-      P r[JB][U];
+    for (int jb = 0; jb < topk; jb += J) {
+      if (topk > J) places(jb);
+      P r[J][U];
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
+      for (int j = 0; j < J; ++j) {
         if (p[j] < 0) continue;
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(256, U == 1 ? 3 : 2)
             r[j][u] = reinterpret_cast<const P*>(ys + (int64_t)p[j] * ldys)[i + u * (int)blockDim.x];
       }
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
+      for (int j = 0; j < J; ++j) {
         if (p[j] < 0) continue;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -384,8 +387,8 @@ __global__ void __launch_bounds__(256, U == 1 ? 3 : 2)
 }
 
 // One CTA per token: the dot products of its experts' rows with dy[t] need
-// the whole row, and dy is read once for JB of them.
-template <typename T, int V, int U>
+// the whole row, and dy is read once for J of them.
+template <typename T, int V, int U, int J>
 __global__ void __launch_bounds__(512)
     combine_grad_kernel(int topk, int64_t S, int64_t nv, const T* __restrict__ dy,
                                     int64_t lddy, const T* __restrict__ ys, int64_t ldys,
@@ -395,27 +398,27 @@ __global__ void __launch_bounds__(512)
   using P = Pack<T, V>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float red[JB][32];
+  __shared__ float red[J][32];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  for (int jb = 0; jb < topk; jb += JB) {
-    int p[JB];
-    float wj[JB], dot[JB];
+  for (int jb = 0; jb < topk; jb += J) {
+    int p[J];
+    float wj[J], dot[J];
 #pragma unroll
-    for (int j = 0; j < JB; ++j) {
+    for (int j = 0; j < J; ++j) {
       p[j] = jb + j < topk ? place_of(pos, t * topk + jb + j, S, status) : -1;
       wj[j] = (w && p[j] >= 0) ? __ldg(w + t * topk + jb + j) : 1.0f;
       dot[j] = 0.0f;
     }
     for (int64_t i = threadIdx.x; i < nv; i += blockDim.x * U) {
-      P g[U], r[JB][U];
+      P g[U], r[J][U];
       const P* from = reinterpret_cast<const P*>(dy + t * lddy) + i;
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (u == 0 || i + u * (int)blockDim.x < nv) g[u] = from[u * (int)blockDim.x];
       if (dw) {
 #pragma unroll
-        for (int j = 0; j < JB; ++j) {
+        for (int j = 0; j < J; ++j) {
           if (p[j] < 0) continue;
           const P* row = reinterpret_cast<const P*>(ys + (int64_t)p[j] * ldys) + i;
 #pragma unroll
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(512)
         float gf[V];
         unpack(g[u], gf);
 #pragma unroll
-        for (int j = 0; j < JB; ++j) {
+        for (int j = 0; j < J; ++j) {
           if (p[j] < 0) continue;
           float v[V];
           if (dw) {
@@ -449,13 +452,13 @@ __global__ void __launch_bounds__(512)
     }
     if (dw) {
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
+      for (int j = 0; j < J; ++j) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
         if (lane == 0) red[j][warp] = dot[j];
       }
       __syncthreads();
-      if (threadIdx.x < JB && jb + (int)threadIdx.x < topk) {
+      if (threadIdx.x < J && jb + (int)threadIdx.x < topk) {
         float s = 0.0f;
         for (int k = 0; k < nw; ++k) s += red[threadIdx.x][k];
         dw[t * topk + jb + threadIdx.x] = s;  // 0 for an entry without an expert
@@ -496,41 +499,67 @@ int row_threads(int64_t nv, int most) {
   return (int)min64(most, max64(32, round_up(nv, 32)));
 }
 
+template <typename T, int V, int J>
+int run_combine_as(int T_, int topk, int64_t S, int N, const void* ys, int64_t ldys,
+                   const int32_t* pos, const float* w, void* y, int64_t ldy, cudaStream_t st) {
+  constexpr int U = in_flight(V * (int)sizeof(T), J);
+  const int64_t nv = N / V;
+  const int th = row_threads(cdiv(nv, U), 256);
+  // a few tokens: several CTAs share a token's row
+  const int parts = (int)max64(1, min64(cdiv(nv, th * U), cdiv(2 * num_sms(), T_)));
+  return launch_pdl(combine_rows_kernel<T, V, U, J>, dim3((unsigned)T_, (unsigned)parts), th, 0, st,
+                    topk, S, nv, (const T*)ys, ldys, pos, w, (T*)y, ldy, status_word());
+}
+
+template <typename T, int V, int J>
+int run_combine_grad_as(int T_, int topk, int64_t S, int N, const void* dy, int64_t lddy,
+                        const void* ys, int64_t ldys, const int32_t* pos, const float* w, void* dys,
+                        int64_t lddys, float* dw, cudaStream_t st) {
+  constexpr int U = in_flight(V * (int)sizeof(T), J);
+  const int64_t nv = N / V;
+  const int th = row_threads(cdiv(nv, U), T_ >= 8 * num_sms() ? 128 : 512);
+  return launch_pdl(combine_grad_kernel<T, V, U, J>, dim3((unsigned)T_), th, 0, st, topk, S, nv,
+                    (const T*)dy, lddy, (const T*)ys, ldys, pos, w, (T*)dys, lddys, dw,
+                    status_word());
+}
+
+// go(V, J), both as types, for `vec` values per access and the experts per
+// step.  4096 tokens of 4096 bf16: topk 4 summed 8 at a time 41.6 us, 4 at a
+// time 32.6; topk 2 36.5 and, 2 at a time, 21.1 (rows of 4091: 68 and 46).
+// With few tokens and narrow accesses a thread with 8 to 16 of them only lasts
+// longer than several threads with 4 (1 token, 2 x 2001: 2.2 and 1.9 us).
+template <typename T, typename F>
+int by_shape(int vec, int T_, int topk, F go) {
+  constexpr int B = (int)sizeof(T);
+  if (T_ < num_sms() && vec * B < 16) topk = 8;
+  auto with = [&](auto v) {
+    if (topk <= 2) return go(v, std::integral_constant<int, 2>());
+    if (topk <= 4) return go(v, std::integral_constant<int, 4>());
+    return go(v, std::integral_constant<int, 8>());
+  };
+  if (vec * B == 16) return with(std::integral_constant<int, 16 / B>());
+  if (vec * B == 8) return with(std::integral_constant<int, 8 / B>());
+  if (vec * B == 4) return with(std::integral_constant<int, 4 / B>());
+  return with(std::integral_constant<int, 1>());
+}
+
 template <typename T>
 int run_combine(int vec, int T_, int topk, int64_t S, int N, const void* ys, int64_t ldys,
                 const int32_t* pos, const float* w, void* y, int64_t ldy, cudaStream_t st) {
-  const int64_t nv = N / vec;
-  const int u = in_flight(vec * (int)sizeof(T));
-  const int th = row_threads(cdiv(nv, u), 256);
-  // a few tokens: several CTAs share a token's row
-  const int parts = (int)max64(1, min64(cdiv(nv, th * u), cdiv(2 * num_sms(), T_)));
-  const dim3 grid((unsigned)T_, (unsigned)parts);
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, th, 0, st, topk, S, nv, (const T*)ys, ldys, pos, w, (T*)y,
-                      ldy, status_word());
-  };
-  constexpr int B = (int)sizeof(T);
-  if (vec * B == 16) return go(combine_rows_kernel<T, 16 / B, in_flight(16)>);
-  if (vec * B == 8) return go(combine_rows_kernel<T, 8 / B, in_flight(8)>);
-  if (vec * B == 4) return go(combine_rows_kernel<T, 4 / B, in_flight(4)>);
-  return go(combine_rows_kernel<T, 1, in_flight(B)>);
+  return by_shape<T>(vec, T_, topk, [&](auto v, auto j) {
+    return run_combine_as<T, decltype(v)::value, decltype(j)::value>(T_, topk, S, N, ys, ldys, pos, w,
+                                                                     y, ldy, st);
+  });
 }
 
 template <typename T>
 int run_combine_grad(int vec, int T_, int topk, int64_t S, int N, const void* dy, int64_t lddy,
                      const void* ys, int64_t ldys, const int32_t* pos, const float* w, void* dys,
                      int64_t lddys, float* dw, cudaStream_t st) {
-  const int64_t nv = N / vec;
-  const int th = row_threads(cdiv(nv, in_flight(vec * (int)sizeof(T))), T_ >= 8 * num_sms() ? 128 : 512);
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, dim3((unsigned)T_), th, 0, st, topk, S, nv, (const T*)dy, lddy,
-                      (const T*)ys, ldys, pos, w, (T*)dys, lddys, dw, status_word());
-  };
-  constexpr int B = (int)sizeof(T);
-  if (vec * B == 16) return go(combine_grad_kernel<T, 16 / B, in_flight(16)>);
-  if (vec * B == 8) return go(combine_grad_kernel<T, 8 / B, in_flight(8)>);
-  if (vec * B == 4) return go(combine_grad_kernel<T, 4 / B, in_flight(4)>);
-  return go(combine_grad_kernel<T, 1, in_flight(B)>);
+  return by_shape<T>(vec, T_, topk, [&](auto v, auto j) {
+    return run_combine_grad_as<T, decltype(v)::value, decltype(j)::value>(
+        T_, topk, S, N, dy, lddy, ys, ldys, pos, w, dys, lddys, dw, st);
+  });
 }
 
 // Values per access that every pointer, stride and the row length allow.
@@ -619,21 +648,25 @@ extern "C" int qg_spread_rows(int T, int topk, int S, int N, int dtype, const vo
   const int64_t rb = (int64_t)N * esz, xb = ldx * esz, sb = ldxs * esz;
   const uintptr_t bits = (uintptr_t)x | (uintptr_t)xs | (uintptr_t)rb | (uintptr_t)xb | (uintptr_t)sb;
   cudaStream_t st = (cudaStream_t)stream;
-  auto go = [&](auto* word) {
-    using W = std::remove_pointer_t<decltype(word)>;
-    constexpr int U = sizeof(W) == 16 ? 2 : 4;
+  auto go = [&](auto word, auto j) {
+    using W = decltype(word);
+    constexpr int J = decltype(j)::value, U = sizeof(W) == 16 && J == 8 ? 2 : 4;
     const int64_t nv = rb / (int64_t)sizeof(W);
     const int th = row_threads(cdiv(nv, U), 256);
     // a few tokens: several CTAs share a token's row
     const int parts = (int)max64(1, min64(cdiv(nv, U * th), cdiv(2 * num_sms(), T)));
-    return launch_pdl(spread_rows_kernel<W, U>, dim3((unsigned)T, (unsigned)parts), th, 0, st, topk, (int64_t)S, nv,
+    return launch_pdl(spread_rows_kernel<W, U, J>, dim3((unsigned)T, (unsigned)parts), th, 0, st, topk, (int64_t)S, nv,
                       (const W*)x, xb / (int64_t)sizeof(W), pos, (W*)xs, sb / (int64_t)sizeof(W),
                       status_word());
   };
-  if (all_aligned(bits, 16)) return go((uint4*)nullptr);
-  if (all_aligned(bits, 8)) return go((uint2*)nullptr);
-  if (all_aligned(bits, 4)) return go((uint32_t*)nullptr);
-  return go((uint16_t*)nullptr);
+  auto with = [&](auto word) {
+    return topk <= 4 && T >= num_sms() ? go(word, std::integral_constant<int, 4>())
+                     : go(word, std::integral_constant<int, 8>());
+  };
+  if (all_aligned(bits, 16)) return with(uint4());
+  if (all_aligned(bits, 8)) return with(uint2());
+  if (all_aligned(bits, 4)) return with(uint32_t());
+  return with(uint16_t());
 }
 
 extern "C" int qg_combine_rows(int T, int topk, int S, int N, int dtype, const void* ys,

@@ -303,3 +303,52 @@ def test_cold_memory(lib, grad):
         assert torch.equal(out.cpu().view(torch.int16), want), k
         assert lib.qg_device_status(True) == 0
         del packed, scales, rows, out, fresh
+
+
+# every access width (16, 8, 4 and 2 bytes), by the length or by where the rows
+# start, with the experts taken 2, 4 and 8 at a time, many tokens and few
+@pytest.mark.parametrize("T,topk", [(200, 1), (200, 2), (170, 4), (160, 5), (151, 11), (5, 2), (3, 9)])
+@pytest.mark.parametrize("N,dtype,shift", [(1024, BF, 0), (1020, BF, 0), (1034, BF, 0), (517, BF, 0),
+                                           (4091, torch.float16, 0), (512, torch.float16, 1),
+                                           (2058, torch.float32, 0), (261, torch.float32, 0),
+                                           (2064, BF, 4), (64, torch.float32, 2), (1, BF, 0)])
+def test_row_widths(lib, T, topk, N, dtype, shift):
+    g = torch.Generator(device="cuda").manual_seed(T * N)
+    S = T * topk + 3
+
+    def rows(n):  # rows that start `shift` elements into aligned memory
+        flat = torch.randn(n * (N + shift) + shift, generator=g, device="cuda").to(dtype)
+        return flat[shift:].view(n, N + shift)[:, :N]
+
+    pos = torch.randperm(S, generator=g, device="cuda")[:T * topk].to(torch.int32).view(T, topk)
+    pos[torch.rand((T, topk), generator=g, device="cuda") < 0.2] = -1
+    x, ys, dy = rows(T), rows(S), rows(T)
+    w = torch.rand((T, topk), generator=g, device="cuda")
+    live = pos >= 0
+    xs = rows(S)
+    before = xs.clone()
+    lib.qg_spread_rows(x, pos, xs)
+    want = before.clone()
+    want[pos[live].long()] = x.repeat_interleave(topk, 0)[live.view(-1)]
+    assert torch.equal(xs, want)
+    eps = torch.finfo(dtype).eps / 2
+    # f32 sums of topk products, one rounding to the rows' type (6e-8: the
+    # step of the smallest fp16 values)
+    y = rows(T)
+    lib.qg_combine_rows(ys, pos, y, weights=w)
+    terms = torch.where(live[..., None], w.double()[..., None] * ys.double()[pos.long().clamp(min=0)], 0.0)
+    ref, A = terms.sum(1), terms.abs().sum(1)
+    inner = topk * 2.0 ** -24 * A
+    assert ((y.double() - ref).abs() <= inner + eps * (ref.abs() + inner) + 6e-8).all()
+    # products rounded to f32, then to the rows' type; f32 sums of N products
+    dys, dw = rows(S), torch.empty_like(w)
+    keep = dys.clone()
+    lib.qg_combine_rows_grad(dy, ys, pos, w, dys, dw)
+    prod = (w.double()[..., None] * dy.double()[:, None])[live]
+    at = pos[live].long()
+    assert ((dys.double()[at] - prod).abs() <= (eps + 2.0 ** -23) * prod.abs() + 6e-8).all()
+    other = torch.ones(S, dtype=torch.bool, device="cuda")
+    other[at] = False
+    assert torch.equal(dys[other], keep[other])
+    dots = torch.where(live[..., None], dy.double()[:, None] * ys.double()[pos.long().clamp(min=0)], 0.0)
+    assert ((dw.double() - dots.sum(2)).abs() <= (N + 1) * 2.0 ** -24 * dots.abs().sum(2)).all()
