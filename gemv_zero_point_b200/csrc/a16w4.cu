@@ -40,6 +40,7 @@ constexpr int KC = 128;           // K per chunk: 4 groups, 64 nibble bytes a ro
 constexpr int RT = 4;             // 16-row tiles of a run and row warp
 constexpr int WROWS = 16 * RT;
 constexpr int D = 2;              // chunks in a warp's ring
+constexpr int kDenseRows = 16;    // tokens that a dense call's only pass can hold
 constexpr int kMinRows = 8;       // fewest weight rows that a CTA takes
 constexpr int kXParts = 16;       // CTAs that prefetch a dense call's rows
 
@@ -690,11 +691,12 @@ int64_t packed_bytes(int N, int K, int format) {
 }
 
 // Few rows per expert stream the weights past warp MMAs, more go to the
-// tensor cores.  One matrix: 16 rows at N = 14336, K = 4096 take 19 us here
-// and 23 there, 32 rows 34 and 24.  Experts (64 of 2048 x 2048): 4 rows each
-// take 62 us both ways, 16 rows 122 and 85.  The host knows the average
-// alone; an expert with more rows than it is right either way.
-bool few_rows(int E, int S) { return cdiv(S, E) <= (E > 1 ? 4 : 16); }
+// tensor cores.  One matrix, at N = 14336, K = 4096: 16 rows take 19 us here
+// and 22 there, 32 rows 34 and 22 (12 rows at 2048 x 2048: 4.6 and 12.7).
+// Experts (64 of 2048 x 2048): 3 rows each take 54 and 75 us, 4 rows 63 and 76,
+// 16 rows 122 and 83.  The host knows the average alone; an expert with more
+// rows than it is right either way.
+bool few_rows(int E, int S) { return cdiv(S, E) <= (E > 1 ? 4 : kDenseRows); }
 
 // Checks of every product: QG_OK when the call can run (S may be 0).
 int product_args(int E, int S, int N, int K, const void* in, int64_t ld_in, int in_cols,
