@@ -864,7 +864,9 @@ const void* kernel_of(int fmt, bool grad, int mode) {
 }
 
 constexpr int kMaxDevices = 64;
-int g_tc_pairs[kMaxDevices];  // CTA pairs that can be resident at once (0: not asked yet)
+// What can be resident at once: CTA pairs, and clusters of 2 << i that share a
+// tile's reduction (a cluster lies within one GPC, so fewer than SMs / size).
+int g_tc_pairs[kMaxDevices], g_tc_clusters[kMaxDevices][3];
 
 }  // namespace
 
@@ -881,27 +883,26 @@ int a16w4_tc_setup() {
       if (cudaFuncSetAttribute(kernel_of(fmt, v >= 3, v % 3), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)tc_smem(kA16W4MaxExperts)) != cudaSuccess)
         return QG_ERR_CUDA;
-  // how many pairs can be resident at once (an SM whose partner is disabled
-  // cannot host one)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QG_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = tc_smem(kA16W4MaxExperts);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int pairs = 0;
-  if (cudaOccupancyMaxActiveClusters(&pairs, kernel_of(QG_W4_F32, false, kPair), &cfg) != cudaSuccess ||
-      pairs < 1)
-    return QG_ERR_CUDA;
-  g_tc_pairs[dev] = pairs;
-  return QG_OK;
+  auto resident = [](int size, const void* kernel, int& count) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = tc_smem(kA16W4MaxExperts);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(&count, kernel, &cfg) == cudaSuccess;
+  };
+  bool ok = resident(2, kernel_of(QG_W4_F32, false, kPair), g_tc_pairs[dev]);
+  for (int i = 0; i < 3; ++i)
+    ok = ok && resident(2 << i, kernel_of(QG_W4_F32, false, kShared), g_tc_clusters[dev][i]);
+  return ok && g_tc_pairs[dev] >= 1 ? QG_OK : QG_ERR_CUDA;
 }
 
 size_t a16w4_tc_workspace(int S, int K, bool gather) {
@@ -975,10 +976,12 @@ int launch_a16w4_tc(const A16W4Call& call, bool grad, void* ws, cudaStream_t st)
   }
   const int64_t most = row_tiles * a.ftiles;
   // A dense call whose tiles leave SMs without work: clusters share each
-  // tile's reduction, two stages or more per CTA.
+  // tile's reduction, two stages or more per CTA, all of them resident at once
+  // (17x2048x2048, 16 tiles: clusters of 8, which take two turns, 13.0 us, of 4
+  // 6.5; 33x512x8192, 4 tiles: 9.1 and 12.9).
   a.splits = 1;
   if (!pair && !c.offsets)
-    while (a.splits < 8 && most * a.splits * 2 <= num_sms() && a.stages >= 4 * a.splits)
+    for (int i = 0; i < 3 && most <= g_tc_clusters[dev][i] && a.stages >= 4 * a.splits; ++i)
       a.splits *= 2;
   cfg.gridDim = dim3(pair ? 2 * (unsigned)min64(g_tc_pairs[dev], most) : (unsigned)(a.splits > 1 ? most * a.splits : min64(num_sms(), most)));
   cfg.blockDim = dim3(THREADS);
