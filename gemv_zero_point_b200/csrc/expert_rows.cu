@@ -41,10 +41,15 @@ namespace {
 constexpr int kSortMaxE = 1024;
 constexpr int EPL = 8;                   // entries per lane
 constexpr int kSortOneWarps = 32;        // one CTA sorts everything
-constexpr int64_t kSortOneMax = kSortOneWarps * 32 * EPL;  // most entries of that form
+constexpr int64_t kSortOneMax = 2048;    // most entries of that form (it could hold 8192)
 constexpr int64_t kSortMax = 1 << 22;    // each CTA reads every chunk's counts
 constexpr int kSortWarps = 16;           // several CTAs
-constexpr int kSortChunk = kSortWarps * 32 * EPL;  // entries per CTA then
+// Entries per CTA then: small chunks while there are few of them, since each CTA
+// reads the counts of all.  E = 64: 8192 entries 5.3 us by chunks of 1024, 6.8
+// of 2048, 11.6 in one CTA; E = 128, 65536 entries: 9.9, 8.3 (4096: 9.9); 262144:
+// 23, 16.4 and, of 4096, 15.4.  2048 entries take 5.7 us in one CTA and 4.9 in two
+// launches, of which the second costs the host 2 us.
+int sort_chunk(int64_t n) { return n <= 32768 ? 1024 : n <= 131072 ? 2048 : kSortWarps * 32 * EPL; }
 
 // Expert of entry i (of n), -1 for none.  n < 2^31, so 32-bit divisions.
 __device__ __forceinline__ int expert_of(const int32_t* ids, int64_t ld, int topk, int64_t i,
@@ -179,13 +184,13 @@ __global__ void __launch_bounds__(kSortOneWarps * 32)
 // Counts of each chunk, for the form with several CTAs.
 __global__ void __launch_bounds__(kSortWarps * 32)
     sort_count_kernel(int64_t n, int topk, int E, const int32_t* __restrict__ ids, int64_t ld,
-                      int32_t* __restrict__ hist) {
+                      int64_t per_cta, int32_t* __restrict__ hist) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ int sort_smem[];
   for (int i = threadIdx.x; i < E; i += blockDim.x) sort_smem[i] = 0;
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t c0 = (int64_t)blockIdx.x * kSortChunk, c1 = min64(n, c0 + kSortChunk);
+  const int64_t c0 = (int64_t)blockIdx.x * per_cta, c1 = min64(n, c0 + per_cta);
   int e[EPL];
 #pragma unroll
   for (int r = 0; r < EPL; ++r)
@@ -599,7 +604,7 @@ extern "C" size_t qg_sort_by_expert_workspace_bytes(int T, int topk, int E) {
   if (T <= 0 || topk <= 0 || E <= 0 || E > kSortMaxE) return 0;
   const int64_t n = (int64_t)T * topk;
   if (n > kSortMax || n <= kSortOneMax) return 0;
-  return (size_t)(cdiv(n, kSortChunk) * E * 4);
+  return (size_t)(cdiv(n, sort_chunk(n)) * E * 4);
 }
 
 extern "C" int qg_sort_by_expert(int T, int topk, int E, const int32_t* ids, int64_t ld_ids,
@@ -624,13 +629,14 @@ extern "C" int qg_sort_by_expert(int T, int topk, int E, const int32_t* ids, int
                       (size_t)(warps * E + E + 1) * 4, st, n, topk, E, ids, ld_ids,
                       (const int32_t*)nullptr, n, offsets, src, pos);
   }
-  const unsigned chunks = (unsigned)cdiv(n, kSortChunk);
+  const int64_t per_cta = sort_chunk(n);
+  const unsigned chunks = (unsigned)cdiv(n, per_cta);
   const int rc2 = launch_pdl(sort_count_kernel, dim3(chunks), kSortWarps * 32, (size_t)E * 4, st,
-                             n, topk, E, ids, ld_ids, (int32_t*)workspace);
+                             n, topk, E, ids, ld_ids, per_cta, (int32_t*)workspace);
   if (rc2 != QG_OK) return rc2;
   return launch_pdl(sort_place_kernel, dim3(chunks), kSortWarps * 32,
                     (size_t)(kSortWarps * E + E + 1) * 4, st, n, topk, E, ids, ld_ids,
-                    (const int32_t*)workspace, (int64_t)kSortChunk, offsets, src, pos);
+                    (const int32_t*)workspace, per_cta, offsets, src, pos);
 }
 
 extern "C" int qg_spread_rows(int T, int topk, int S, int N, int dtype, const void* x,

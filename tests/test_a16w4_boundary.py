@@ -105,12 +105,14 @@ def test_workspaces():
     assert experts(**many, ws=None, ws_bytes=need) == WORKSPACE
     assert experts(**many, ws=A + 128, ws_bytes=need) == MISALIGNED
     sb = lib.qg_sort_by_expert_workspace_bytes
-    assert sb(8, 8, 64) == 0 and sb(1024, 8, 64) == 0
-    assert sb(1025, 8, 64) == 3 * 64 * 4             # chunks of 4096 entries
+    assert sb(8, 8, 64) == 0 and sb(256, 8, 64) == 0
+    assert sb(257, 8, 64) == 3 * 64 * 4              # chunks of 1024 entries
+    assert sb(4097, 8, 64) == 17 * 64 * 4            # of 2048
+    assert sb(16385, 8, 64) == 33 * 64 * 4           # of 4096
     assert sb(0, 8, 64) == 0 and sb(8, 8, 1025) == 0 and sb(1 << 22, 2, 4) == 0
-    assert sort(T=1025, topk=8, ld=8, E=64) == WORKSPACE
-    assert sort(T=1025, topk=8, ld=8, E=64, ws=A, ws_bytes=3 * 64 * 4 - 1) == WORKSPACE
-    assert sort(T=1025, topk=8, ld=8, E=64, ws=A + 2, ws_bytes=4096) == MISALIGNED
+    assert sort(T=257, topk=8, ld=8, E=64) == WORKSPACE
+    assert sort(T=257, topk=8, ld=8, E=64, ws=A, ws_bytes=3 * 64 * 4 - 1) == WORKSPACE
+    assert sort(T=257, topk=8, ld=8, E=64, ws=A + 2, ws_bytes=4096) == MISALIGNED
 
 
 def test_sort_refusals():

@@ -352,3 +352,25 @@ def test_row_widths(lib, T, topk, N, dtype, shift):
     assert torch.equal(dys[other], keep[other])
     dots = torch.where(live[..., None], dy.double()[:, None] * ys.double()[pos.long().clamp(min=0)], 0.0)
     assert ((dw.double() - dots.sum(2)).abs() <= (N + 1) * 2.0 ** -24 * dots.abs().sum(2)).all()
+
+
+# both sides of every switch between one CTA and chunks of 1024, 2048 and 4096
+@pytest.mark.parametrize("T,topk,E", [(255, 8, 64), (256, 8, 64), (257, 8, 64), (1024, 3, 1024), (4096, 8, 60),
+                                      (4097, 8, 60), (16384, 8, 1024), (16385, 8, 3), (524288, 8, 256)])
+def test_order_across_chunks(lib, T, topk, E):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    ids = torch.randint(-2, E + 2, (T, topk + 3), generator=g, device="cuda", dtype=torch.int32)[:, :topk]
+    offsets = torch.empty(E + 1, device="cuda", dtype=torch.int32)
+    src = torch.full((T * topk,), -7, device="cuda", dtype=torch.int32)
+    pos = torch.empty((T, topk), device="cuda", dtype=torch.int32)
+    lib.qg_sort_by_expert(ids, offsets, src, pos)
+    flat = ids.reshape(-1).long()
+    key = torch.where((flat >= 0) & (flat < E), flat, E)
+    order = torch.argsort(key, stable=True)
+    want = torch.searchsorted(key[order].contiguous(), torch.arange(E + 1, device="cuda")).int()
+    n = int(want[-1])
+    assert torch.equal(offsets, want)
+    assert torch.equal(src[:n].long(), order[:n]) and (src[n:] == -7).all()
+    places = torch.full((T * topk,), -1, device="cuda", dtype=torch.int32)
+    places[order[:n]] = torch.arange(n, device="cuda", dtype=torch.int32)
+    assert torch.equal(pos.view(-1), places)
