@@ -154,6 +154,32 @@ def _empty_bytes(n, device):
     return torch.empty(max(int(n), 1), dtype=torch.uint8, device=device)
 
 
+def _scratch(n, device, stream):
+    """Workspace of a call on `stream` (None: the current one), dropped when
+    the call returns.  It is allocated under that stream: the allocator hands
+    a dropped block on to work of the stream that it was allocated under, which
+    on another stream could start before the call has read it."""
+    if stream is None or device.type != "cuda":
+        return _empty_bytes(n, device)
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return _empty_bytes(n, device)
+
+
+def _result(n, device, stream):
+    """Memory that a call on `stream` fills and returns: as a workspace, and
+    marked as used on the current stream too, whose later work may read it."""
+    import torch
+    t = _scratch(n, device, stream)
+    if stream is not None and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 # ---------------------------------------------------------------------------
 # Status and requant parameters
 # ---------------------------------------------------------------------------
@@ -219,7 +245,7 @@ def pack_w4_g32(w, group_scales, packed=None, stream=None, bf16_scales=False):
     pack_fn = lib.pack_w4_g32_bf16 if bf16_scales else lib.pack_w4_g32
     nbytes = bytes_fn(N, K)
     if packed is None:
-        packed = _empty_bytes(nbytes, w.device)
+        packed = _result(nbytes, w.device, stream)
     _check(pack_fn(N, K, _p(w), _ld(w), _p(group_scales), _p(packed), packed.numel(),
                    _stream(stream)), pack_fn.__name__)
     return packed
@@ -239,7 +265,7 @@ def qgemm_a8w4_f32(x, packed_w, N, bias, clamp_min, clamp_max, y, q_out=None, sc
     M, K = x.shape
     wsb = lib.qgemm_a8w4_workspace_bytes(M, N, K)
     if wsb and workspace is None:
-        workspace = _empty_bytes(wsb, x.device)
+        workspace = _scratch(wsb, x.device, stream)
     fn = lib.qgemm_a8w4_f32_bf16s if bf16_scales else lib.qgemm_a8w4_f32
     _check(fn(M, N, K, _p(x), _ld(x), _p(packed_w), _p(bias),
               float(clamp_min), float(clamp_max), _p(y), _ld(y), _p(q_out),
@@ -247,10 +273,10 @@ def qgemm_a8w4_f32(x, packed_w, N, bias, clamp_min, clamp_max, y, q_out=None, sc
               0 if workspace is None else workspace.numel(), _stream(stream)), fn.__name__)
 
 
-def _a8w4_workspace(M, N, K, workspace, device):
+def _a8w4_workspace(M, N, K, workspace, device, stream):
     wsb = lib.qgemm_a8w4_workspace_bytes(M, N, K)
     if wsb and workspace is None:
-        workspace = _empty_bytes(wsb, device)
+        workspace = _scratch(wsb, device, stream)
     return workspace
 
 
@@ -259,7 +285,7 @@ def qgemm_a8w4_f32_actblock(x, packed_w, N, bias, clamp_min, clamp_max, y, q_out
     """A8W4 linear with the activations quantized per 32-wide K block;
     scale_out / zp_out, when given, receive [M][K/32] values."""
     M, K = x.shape
-    workspace = _a8w4_workspace(M, N, K, workspace, x.device)
+    workspace = _a8w4_workspace(M, N, K, workspace, x.device, stream)
     _check(lib.qgemm_a8w4_f32_actblock(M, N, K, _p(x), _ld(x), _p(packed_w), _p(bias),
                                        float(clamp_min), float(clamp_max), _p(y), _ld(y),
                                        _p(q_out), _p(scale_out), _p(zp_out), _p(workspace),
@@ -272,7 +298,7 @@ def pack_w4_g32_asym(w, group_scales, group_zeros, packed=None, stream=None):
     """Pack int4 weights with f32 group scales and f32 group zeros."""
     N, K = w.shape
     if packed is None:
-        packed = _empty_bytes(lib.pack_w4_g32_asym_bytes(N, K), w.device)
+        packed = _result(lib.pack_w4_g32_asym_bytes(N, K), w.device, stream)
     _check(lib.pack_w4_g32_asym(N, K, _p(w), _ld(w), _p(group_scales), _p(group_zeros),
                                 _p(packed), packed.numel(), _stream(stream)), "pack_w4_g32_asym")
     return packed
@@ -282,7 +308,7 @@ def qgemm_a8w4_f32_asym(x, packed_w, N, bias, clamp_min, clamp_max, y, q_out=Non
                         scale_out=None, zp_out=None, workspace=None, stream=None):
     """A8W4 linear with asymmetric int4 weights (pack_w4_g32_asym)."""
     M, K = x.shape
-    workspace = _a8w4_workspace(M, N, K, workspace, x.device)
+    workspace = _a8w4_workspace(M, N, K, workspace, x.device, stream)
     _check(lib.qgemm_a8w4_f32_asym(M, N, K, _p(x), _ld(x), _p(packed_w), _p(bias),
                                    float(clamp_min), float(clamp_max), _p(y), _ld(y),
                                    _p(q_out), _p(scale_out), _p(zp_out), _p(workspace),
@@ -307,7 +333,7 @@ def qgemm_pack_b_s8(B, N=None, packed=None, stream=None):
     N = B.shape[1] if N is None else N
     nbytes = lib.qgemm_pack_b_s8_bytes(K, N)
     if packed is None:
-        packed = _empty_bytes(nbytes, B.device)
+        packed = _result(nbytes, B.device, stream)
     _check(lib.qgemm_pack_b_s8(K, N, _p(B), _ld(B), _p(packed), packed.numel(), _stream(stream)),
            "qgemm_pack_b_s8")
     return packed
@@ -327,7 +353,7 @@ def qgemm_s8s8_requant(A, B, C, rq, K=None, N=None, acc_out=None, workspace=None
     N = C.shape[1] if N is None else N
     wsb = lib.qgemm_s8s8_workspace_bytes(M, N, K)
     if workspace is None:
-        workspace = _empty_bytes(wsb, A.device)
+        workspace = _scratch(wsb, A.device, stream)
     _check(lib.qgemm_s8s8_requant(M, N, K, _p(A), _ld(A), _p(B), _ld(B), _p(C), _ld(C),
                                   ctypes.byref(rq), _p(acc_out),
                                   0 if acc_out is None else _ld(acc_out), _p(workspace),
@@ -340,7 +366,7 @@ def qgemm_s8s8_requant_packed(A, packed_b, N, C, rq, K=None, acc_out=None, works
     K = A.shape[1] if K is None else K
     wsb = lib.qgemm_s8s8_packed_workspace_bytes(M, K)
     if workspace is None:
-        workspace = _empty_bytes(wsb, A.device)
+        workspace = _scratch(wsb, A.device, stream)
     _check(lib.qgemm_s8s8_requant_packed(M, N, K, _p(A), _ld(A), _p(packed_b), _p(C), _ld(C),
                                          ctypes.byref(rq), _p(acc_out),
                                          0 if acc_out is None else _ld(acc_out), _p(workspace),
@@ -365,7 +391,7 @@ def qconv2d_s8_im2col(x, w, y, rq, stride, pad, acc_out=None, workspace=None, st
     assert Cin == Cin2 and x.is_contiguous() and w.is_contiguous() and y.is_contiguous()
     wsb = qconv2d_s8_workspace_bytes(x.shape, w.shape, stride, pad)
     if workspace is None:
-        workspace = _empty_bytes(wsb, x.device)
+        workspace = _scratch(wsb, x.device, stream)
     _check(lib.qconv2d_s8_im2col(Nb, H, W, Cin, Cout, KH, KW, stride[0], stride[1], pad[0],
                                  pad[1], _p(x), _p(w), _p(y), ctypes.byref(rq), _p(acc_out),
                                  _p(workspace), workspace.numel(), _stream(stream)),
@@ -377,7 +403,7 @@ def qconv2d_s8_pack_w(w, packed=None, stream=None):
     Cout, KH, KW, Cin = w.shape
     assert w.is_contiguous()
     if packed is None:
-        packed = _empty_bytes(lib.qconv2d_s8_pack_w_bytes(Cout, KH, KW, Cin), w.device)
+        packed = _result(lib.qconv2d_s8_pack_w_bytes(Cout, KH, KW, Cin), w.device, stream)
     _check(lib.qconv2d_s8_pack_w(Cout, KH, KW, Cin, _p(w), _p(packed), packed.numel(),
                                  _stream(stream)), "qconv2d_s8_pack_w")
     return packed
@@ -417,8 +443,8 @@ def qconv2d_f32_dyn_a8w4(x, packed_w, Cout, KH, KW, stride, pad, bias, clamp_min
     Nb, H, W, Cin = x.shape
     assert x.is_contiguous() and y.is_contiguous()
     if workspace is None:
-        workspace = _empty_bytes(qconv2d_f32_dyn_a8w4_workspace_bytes(x.shape, Cout, KH, KW,
-                                                                      stride, pad), x.device)
+        workspace = _scratch(qconv2d_f32_dyn_a8w4_workspace_bytes(x.shape, Cout, KH, KW, stride, pad),
+                             x.device, stream)
     _check(lib.qconv2d_f32_dyn_a8w4(Nb, H, W, Cin, Cout, KH, KW, stride[0], stride[1], pad[0],
                                     pad[1], _p(x), _p(packed_w), _p(bias), float(clamp_min),
                                     float(clamp_max), 1 if symmetric else 0, _p(y), _p(q_out),
@@ -564,7 +590,7 @@ def qgemm_a16w4_bf16_experts(x, offsets, packed_w, y, src=None, topk=1, bias=Non
     elif src is not None:
         have = lib.qgemm_a16w4_bf16_experts_workspace_bytes(E, S, K, 1)
         if have:
-            workspace = _empty_bytes(have, x.device)
+            workspace = _scratch(have, x.device, stream)
     _launch(lib.qgemm_a16w4_bf16_experts, stream, x.get_device(),
             (offsets, packed_w, y, src, bias, workspace),
             (E, S, N, K, x.data_ptr(), ldx, rows, _addr(src), topk, offsets.data_ptr(),
@@ -618,7 +644,7 @@ def qg_sort_by_expert(ids, offsets, src, pos, workspace=None, stream=None):
     if workspace is None:
         have = lib.qg_sort_by_expert_workspace_bytes(T, topk, E)
         if have:
-            workspace = _empty_bytes(have, ids.device)
+            workspace = _scratch(have, ids.device, stream)
     else:
         have = _workspace_size(workspace)
     _launch(lib.qg_sort_by_expert, stream, ids.get_device(), (offsets, src, pos, workspace),

@@ -1,0 +1,165 @@
+"""Calls on a stream other than the current one, through the `stream` argument:
+what a call allocates for itself belongs to the stream that it runs on."""
+import numpy as np
+import pytest
+
+import a16w4_cases as C
+import oracle
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(autouse=True)
+def _clean_status(lib, cuda):
+    lib.qg_device_status(True)
+    yield
+    assert lib.qg_device_status(True) == 0
+
+
+def _i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()
+
+
+class Experts:
+    """Indirect rows, many per expert: the sorted rows lie in a workspace."""
+    T, topk, E, N, K = 600, 2, 4, 136, 320
+
+    def __init__(self, lib, seed):
+        rng = np.random.default_rng(seed)
+        self.lib = lib
+        qw, sw, zw = C.weights(rng, self.N, self.K, "f32", self.E)
+        ids = C.routing(rng, self.T, self.topk, self.E)
+        offsets, src, _ = oracle.sort_by_expert(ids, self.E)
+        self.packed = C.pack_experts(lib, torch, qw, sw, zw, "f32")
+        self.offsets, self.src = _i32(offsets), _i32(src)
+        self.x = torch.from_numpy(C.bf16_round(rng.standard_normal((self.T, self.K)))).cuda().to(BF)
+        self.y = torch.zeros((self.T * self.topk, self.N), dtype=BF, device="cuda")
+
+    def __call__(self, stream=None):
+        self.lib.qgemm_a16w4_bf16_experts(self.x, self.offsets, self.packed, self.y, src=self.src,
+                                          topk=self.topk, stream=stream)
+
+    def result(self):
+        return [self.y.view(torch.int16)]
+
+
+class Order:
+    """More entries than one CTA sorts: the chunks' counts lie in a workspace."""
+    T, topk, E = 3000, 4, 300
+
+    def __init__(self, lib, seed):
+        self.lib = lib
+        self.ids = _i32(np.random.default_rng(seed).integers(0, self.E, (self.T, self.topk)))
+        self.offsets, self.src, self.pos = _i32(np.zeros(self.E + 1)), _i32(np.zeros(self.T * self.topk)), \
+            _i32(np.zeros((self.T, self.topk)))
+
+    def __call__(self, stream=None):
+        self.lib.qg_sort_by_expert(self.ids, self.offsets, self.src, self.pos, stream=stream)
+
+    def result(self):
+        return [self.offsets, self.src, self.pos]
+
+
+class A8W4:
+    """Quantized activations between two kernels lie in a workspace."""
+    M, N, K = 96, 200, 512
+
+    def __init__(self, lib, seed):
+        rng = np.random.default_rng(seed)
+        self.lib = lib
+        qw, sw, _ = C.weights(rng, self.N, self.K, "f32")
+        self.packed = C.pack(lib, torch, qw, sw, None, "f32")
+        self.x = torch.from_numpy(rng.standard_normal((self.M, self.K)).astype(np.float32)).cuda()
+        self.bias = torch.zeros(self.N, device="cuda")
+        self.y = torch.zeros((self.M, self.N), device="cuda")
+
+    def __call__(self, stream=None):
+        self.lib.qgemm_a8w4_f32(self.x, self.packed, self.N, self.bias, -1e30, 1e30, self.y,
+                                stream=stream)
+
+    def result(self):
+        return [self.y]
+
+
+CALLS = [Experts, Order, A8W4]
+
+
+@pytest.mark.parametrize("kind", CALLS)
+@pytest.mark.parametrize("raw", [False, True])
+def test_workspace_belongs_to_the_calls_stream(lib, monkeypatch, kind, raw):
+    """While the call still waits on its stream, its workspace is not handed
+    out to the current one."""
+    call = kind(lib, 1)
+    call()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    seen, real = [], lib._empty_bytes
+
+    def spy(n, device):
+        t = real(n, device)
+        seen.append((t.data_ptr(), t.numel()))
+        return t
+    monkeypatch.setattr(lib, "_empty_bytes", spy)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    call(stream=side.cuda_stream if raw else side)
+    assert len(seen) == 1, "the call was to need a workspace"
+    at, n = seen[0]
+    others = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert not side.query(), "the call had ended before the check"
+    assert all(t.data_ptr() >= at + n or t.data_ptr() + n <= at for t in others)
+    torch.cuda.synchronize()
+
+
+def test_packed_weights_of_another_stream(lib, monkeypatch):
+    """A matrix packed on another stream: its memory is not handed out before
+    that stream, or the current one, is done with it."""
+    rng = np.random.default_rng(3)
+    qw, sw, _ = C.weights(rng, 264, 1024, "f32")
+    q, s = torch.from_numpy(qw).cuda(), torch.from_numpy(sw).cuda()
+    want = lib.pack_w4_g32(q, s)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    packed = lib.pack_w4_g32(q, s, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(50_000_000)
+    same = torch.equal(packed, want)  # waits
+    at, n = packed.data_ptr(), packed.numel()
+    copy = torch.empty_like(packed)
+    torch.cuda._sleep(50_000_000)
+    copy.copy_(packed)
+    del packed
+    with torch.cuda.stream(side):
+        others = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        for t in others:
+            t.fill_(255)
+    assert same and all(t.data_ptr() >= at + n or t.data_ptr() + n <= at for t in others)
+    assert torch.equal(copy, want)
+
+
+@pytest.mark.parametrize("kind", CALLS)
+def test_two_calls_on_two_streams(lib, kind):
+    """Calls on two explicit streams, neither the current one, many times
+    over: the bits of the same calls one after the other."""
+    calls = [kind(lib, k) for k in range(2)]
+    want = []
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in call.result()])
+        for t in call.result():
+            t.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for call, stream in zip(calls, streams):
+            call(stream=stream)
+        junk = torch.full((1 << 21,), 0xFF, dtype=torch.uint8, device="cuda")
+        del junk
+    torch.cuda.synchronize()
+    for call, ref in zip(calls, want):
+        assert all(torch.equal(a, b) for a, b in zip(call.result(), ref))
