@@ -815,7 +815,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Rows into sorted order: xs[p] = x[src[p] / topk] for the rows that belong
-// to an expert, a warp per row.
+// to an expert, a warp per row.  The work before the call may write them while
+// this kernel is resident, so they are read by ordinary loads, not as constants.
 __global__ void __launch_bounds__(256) a16w4_gather_kernel(const __grid_constant__ A16W4Call c,
                                                            uint16_t* __restrict__ xs, int* status) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -837,11 +838,11 @@ __global__ void __launch_bounds__(256) a16w4_gather_kernel(const __grid_constant
   for (; i + 96 < nv; i += 128) {
     uint4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __ldg(from + i + 32 * k);
+    for (int k = 0; k < 4; ++k) v[k] = from[i + 32 * k];
 #pragma unroll
     for (int k = 0; k < 4; ++k) dst[i + 32 * k] = v[k];
   }
-  for (; i < nv; i += 32) dst[i] = __ldg(from + i);
+  for (; i < nv; i += 32) dst[i] = from[i];
 }
 
 // ---------------------------------------------------------------------------

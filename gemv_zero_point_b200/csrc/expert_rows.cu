@@ -13,6 +13,12 @@
 // sorted rows) lets a token's row be read once for its topk copies, and lets
 // combine's gradient read dy once for all of a token's experts.  Sums are
 // held in f32 and rounded once.
+//
+// Every kernel becomes resident while the work before it may still be writing
+// its inputs.  They are not constant over the kernel's life, so they are read by
+// ordinary loads behind griddepcontrol.wait: no __ldg and no __restrict__ on
+// an input, either of which lets a load go through the path for constants, or
+// ahead of the wait.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -109,8 +115,8 @@ __device__ __forceinline__ uint32_t peers_of(int e, int bits) {
 // hist == NULL: one CTA holds every entry.  Otherwise hist[chunks][E] holds
 // each chunk's counts and this CTA places chunk blockIdx.x.
 __global__ void __launch_bounds__(kSortOneWarps * 32)
-    sort_place_kernel(int64_t n, int topk, int E, const int32_t* __restrict__ ids, int64_t ld,
-                      const int32_t* __restrict__ hist, int64_t per_cta,
+    sort_place_kernel(int64_t n, int topk, int E, const int32_t* ids, int64_t ld,
+                      const int32_t* hist, int64_t per_cta,
                       int32_t* __restrict__ offsets, int32_t* __restrict__ src,
                       int32_t* __restrict__ pos) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -183,7 +189,7 @@ __global__ void __launch_bounds__(kSortOneWarps * 32)
 
 // Counts of each chunk, for the form with several CTAs.
 __global__ void __launch_bounds__(kSortWarps * 32)
-    sort_count_kernel(int64_t n, int topk, int E, const int32_t* __restrict__ ids, int64_t ld,
+    sort_count_kernel(int64_t n, int topk, int E, const int32_t* ids, int64_t ld,
                       int64_t per_cta, int32_t* __restrict__ hist) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ int sort_smem[];
@@ -277,15 +283,20 @@ __device__ __forceinline__ void pack(const float (&f)[1], Pack<__nv_bfloat16, 1>
   p.w[0] = __float2bfloat16_rn(f[0]);
 }
 
-// Sorted position of (t, j), or -1 when the entry has no expert.  A position
-// outside [0, S) is an error of the caller's: recorded, then treated as -1.
-__device__ __forceinline__ int place_of(const int32_t* pos, int64_t i, int64_t S, int* status) {
-  const int p = __ldg(pos + i);
-  if (p >= S) {
-    record_error(status, QG_ERR_INVALID_ARG);
-    return -1;
-  }
-  return p < 0 ? -1 : p;
+// Sorted positions of J entries from pos on, of which there are n; negative
+// ones have no expert.  A position outside [0, S) is an error of the caller's:
+// recorded, then treated as -1.  All loads come before the checks: a load
+// behind one check and ahead of the next would wait for it.
+template <int J>
+__device__ __forceinline__ void places_of(const int32_t* pos, int n, int64_t S, int* status, int (&p)[J]) {
+#pragma unroll
+  for (int j = 0; j < J; ++j) p[j] = j < n ? pos[j] : -1;
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+    if (p[j] >= S) {
+      record_error(status, QG_ERR_INVALID_ARG);
+      p[j] = -1;
+    }
 }
 
 // J experts of a token are taken together: 8, or 4 or 2 where topk is no more.
@@ -298,8 +309,8 @@ constexpr int in_flight(int bytes, int J) {
 
 template <typename W, int U, int J>
 __global__ void __launch_bounds__(256, 4)
-    spread_rows_kernel(int topk, int64_t S, int64_t nv, const W* __restrict__ x, int64_t ldx,
-                       const int32_t* __restrict__ pos, W* __restrict__ xs, int64_t ldxs,
+    spread_rows_kernel(int topk, int64_t S, int64_t nv, const W* x, int64_t ldx,
+                       const int32_t* pos, W* __restrict__ xs, int64_t ldxs,
                        int* status) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -308,10 +319,8 @@ __global__ void __launch_bounds__(256, 4)
   const int64_t i0 = (int64_t)blockIdx.y * blockDim.x * U + threadIdx.x;
   const int64_t step = (int64_t)gridDim.y * blockDim.x * U;
   for (int jb = 0; jb < topk; jb += J) {
-    int64_t p[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      p[j] = jb + j < topk ? place_of(pos, t * topk + jb + j, S, status) : -1;
+    int p[J];
+    places_of(pos + t * topk + jb, topk - jb, S, status, p);
     for (int64_t i = i0; i < nv; i += step) {
       W a[U];
 #pragma unroll
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(256, 4)
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         if (p[j] < 0) continue;
-        W* d = xs + p[j] * ldxs;
+        W* d = xs + (int64_t)p[j] * ldxs;
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (i + u * (int)blockDim.x < nv) d[i + u * (int)blockDim.x] = a[u];
@@ -334,8 +343,8 @@ __global__ void __launch_bounds__(256, 4)
 // (8192 tokens x 8 rows of 4096 bf16: 282 us).
 template <typename T, int V, int U, int J>
 __global__ void __launch_bounds__(256, U == 1 ? 3 : 2)
-    combine_rows_kernel(int topk, int64_t S, int64_t nv, const T* __restrict__ ys, int64_t ldys,
-                        const int32_t* __restrict__ pos, const float* __restrict__ w,
+    combine_rows_kernel(int topk, int64_t S, int64_t nv, const T* ys, int64_t ldys,
+                        const int32_t* pos, const float* w,
                         T* __restrict__ y, int64_t ldy, int* status) {
   using P = Pack<T, V>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -346,10 +355,8 @@ __global__ void __launch_bounds__(256, U == 1 ? 3 : 2)
   float wj[J];
   auto places = [&](int jb) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      p[j] = jb + j < topk ? place_of(pos, t * topk + jb + j, S, status) : -1;
-      wj[j] = w && p[j] >= 0 ? __ldg(w + t * topk + jb + j) : 1.0f;
-    }
+    for (int j = 0; j < J; ++j) wj[j] = w && jb + j < topk ? w[t * topk + jb + j] : 1.0f;
+    places_of(pos + t * topk + jb, topk - jb, S, status, p);
   };
   if (topk <= J) places(0);
   for (int64_t i = (int64_t)blockIdx.y * blockDim.x * U + threadIdx.x; i < nv; i += step) {
@@ -395,9 +402,9 @@ __global__ void __launch_bounds__(256, U == 1 ? 3 : 2)
 // the whole row, and dy is read once for J of them.
 template <typename T, int V, int U, int J>
 __global__ void __launch_bounds__(512)
-    combine_grad_kernel(int topk, int64_t S, int64_t nv, const T* __restrict__ dy,
-                                    int64_t lddy, const T* __restrict__ ys, int64_t ldys,
-                                    const int32_t* __restrict__ pos, const float* __restrict__ w,
+    combine_grad_kernel(int topk, int64_t S, int64_t nv, const T* dy,
+                                    int64_t lddy, const T* ys, int64_t ldys,
+                                    const int32_t* pos, const float* w,
                                     T* __restrict__ dys, int64_t lddys, float* __restrict__ dw,
                                     int* status) {
   using P = Pack<T, V>;
@@ -411,10 +418,10 @@ __global__ void __launch_bounds__(512)
     float wj[J], dot[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      p[j] = jb + j < topk ? place_of(pos, t * topk + jb + j, S, status) : -1;
-      wj[j] = (w && p[j] >= 0) ? __ldg(w + t * topk + jb + j) : 1.0f;
+      wj[j] = w && jb + j < topk ? w[t * topk + jb + j] : 1.0f;
       dot[j] = 0.0f;
     }
+    places_of(pos + t * topk + jb, topk - jb, S, status, p);
     for (int64_t i = threadIdx.x; i < nv; i += blockDim.x * U) {
       P g[U], r[J][U];
       const P* from = reinterpret_cast<const P*>(dy + t * lddy) + i;

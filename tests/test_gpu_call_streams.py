@@ -160,3 +160,55 @@ def test_two_calls_on_two_streams(lib, kind):
     torch.cuda.synchronize()
     for call, ref in zip(calls, want):
         assert all(torch.equal(a, b) for a, b in zip(call.result(), ref))
+
+
+@pytest.mark.parametrize("T,topk,N", [(16, 8, 256), (16, 2, 4096), (130, 4, 520), (700, 4, 64)])
+@pytest.mark.parametrize("grad", [False, True])
+def test_steps_behind_one_another_share_their_buffers(lib, T, topk, N, grad):
+    """Steps of order, spread and sum back to back in one graph, with other ids
+    each and the same places and rows: a kernel is resident while the one
+    before it still reads the last step's places and writes this step's, and
+    must not see the old ones.  Every step's own results are kept."""
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    steps, E, S = 24, 64, T * topk
+    ids = torch.randint(0, E, (steps, T, topk), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn((steps, T, N), generator=g, device="cuda").to(BF)
+    w = torch.rand((steps, T, topk), generator=g, device="cuda")
+    offsets, src, pos = (torch.empty(n, device="cuda", dtype=torch.int32) for n in (E + 1, S, S))
+    pos = pos.view(T, topk)
+    xs, dys = torch.empty((S, N), device="cuda", dtype=BF), torch.empty((S, N), device="cuda", dtype=BF)
+    wk, dw = torch.empty((T, topk), device="cuda"), torch.empty((steps, T, topk), device="cuda")
+    y = torch.empty_like(x)
+
+    def run():
+        for k in range(steps):
+            lib.qg_sort_by_expert(ids[k], offsets, src, pos)
+            lib.qg_spread_rows(x[k], pos, xs)
+            if grad:  # of the sum, and the spread's own: two kernels read the places
+                lib.qg_combine_rows_grad(x[k], xs, pos, w[k], dys, dw[k])
+                lib.qg_combine_rows(dys, pos, y[k])
+            else:
+                lib.qg_combine_rows(xs, pos, y[k], weights=w[k])
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(5):
+        y.zero_()
+        pos.fill_(-1)
+        graph.replay()
+        torch.cuda.synchronize()
+        xd, wd = x.double(), w.double()
+        if grad:
+            # products rounded to bf16, f32 sums of topk of them, rounded to bf16
+            terms = wd[..., None] * xd[:, :, None]
+            A = terms.abs().sum(2)
+            assert ((y.double() - terms.sum(2)).abs() <= (2.0 ** -7 + 2.0 ** -14) * A + 1e-30).all()
+            # f32 sums of N products
+            dots = (xd * xd).sum(-1)
+            assert ((dw.double() - dots[..., None]).abs() <= (N + 1) * 2.0 ** -24 * dots[..., None]).all()
+        else:
+            # f32 sums of topk products, rounded to bf16
+            ref, A = wd.sum(2)[..., None] * xd, wd.sum(2)[..., None] * xd.abs()
+            assert ((y.double() - ref).abs() <= (2.0 ** -8 + topk * 2.0 ** -22) * A + 1e-30).all()
