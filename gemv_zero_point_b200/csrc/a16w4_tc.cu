@@ -814,6 +814,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+// Does row p lie in a range of offsets that expert_range takes?  One warp asks.
+__device__ __forceinline__ bool in_some_range(const A16W4Call& c, int p, int lane) {
+  // the ranges of sorted offsets cover [offsets[0], offsets[E]); with unsorted
+  // ones that may hold rows of nobody, which nobody reads
+  if (p >= c.offsets[0] && p < min(c.offsets[c.E], c.S)) return true;
+  // behind the last row in ordinary calls; with unsorted offsets a range may
+  // lie there all the same
+  bool in = false;
+  for (int e = lane; e < c.E; e += 32) {
+    const int2 r = expert_range(c.offsets, e, c.S, nullptr);
+    in |= p >= r.x && p - r.x < r.y;
+  }
+  return __any_sync(0xffffffffu, in);
+}
+
 // Rows into sorted order: xs[p] = x[src[p] / topk] for the rows that belong
 // to an expert, a warp per row.  The work before the call may write them while
 // this kernel is resident, so they are read by ordinary loads, not as constants.
@@ -822,8 +837,9 @@ __global__ void __launch_bounds__(256) a16w4_gather_kernel(const __grid_constant
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int p = (int)(blockIdx.x * 8 + (threadIdx.x >> 5));
-  if (p < c.offsets[0] || p >= min(c.offsets[c.E], c.S)) return;
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (at >= c.S || !in_some_range(c, (int)at, lane)) return;
+  const int p = (int)at;
   const int s = c.src[p];
   const int row = s < 0 ? c.in_rows : s / c.topk;
   const int nv = c.K / 8;  // K % 64 == 0 and 16-byte aligned rows
