@@ -228,13 +228,14 @@ struct Scale<QG_W4_BF16> {
   uint32_t s;
 };
 // f32 scales: s = hi + lo in bf16; fma(code, hi, code * lo) rounds the sum
-// once (lo's own rounding is 2^-17 of s)
+// once (the roundings of lo and of code * lo are below 2^-15 of the weight)
 template <>
 struct Scale<QG_W4_F32> {
   uint32_t hi, lo;
 };
-// f32 scales and zeros: s * (128 + u) + (z - 136 s) in f32, rounded to bf16
-// (the rounding of z - 136 s is 2^-17 of s at most)
+// f32 scales and zeros: fma(s, code, z) in f32, rounded to bf16.  The code
+// itself is the factor: with 128 + u as it is unpacked, the rounding of z - 136 s
+// would stay where s * code and z cancel.
 template <>
 struct Scale<QG_W4_ASYM> {
   float s, z;
@@ -249,6 +250,25 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
   uint32_t d;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
+}
+
+__device__ __forceinline__ uint64_t pair_bits(float2 a) {
+  return (uint64_t)__float_as_uint(a.y) << 32 | __float_as_uint(a.x);
+}
+__device__ __forceinline__ float2 pair_of(uint64_t a) {
+  return make_float2(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)));
+}
+__device__ __forceinline__ float2 f32x2_add(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return pair_of(d);
+}
+__device__ __forceinline__ float2 f32x2_fma(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return pair_of(d);
 }
 
 // Raw stored scales (and zeros, zoff bytes further) of two neighbouring
@@ -285,7 +305,7 @@ __device__ __forceinline__ Scale<FMT> make_scale(const RawScales& v, int i) {
     s.lo = lo | (lo << 16);
   } else {
     s.s = __uint_as_float(raw);
-    s.z = fmaf(-136.0f, s.s, __uint_as_float(i ? v.z.y : v.z.x));
+    s.z = __uint_as_float(i ? v.z.y : v.z.x);
   }
   return s;
 }
@@ -298,11 +318,11 @@ __device__ __forceinline__ void expand8(uint32_t w, const Scale<FMT>& s, uint32_
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t b = i < 2 ? L : H;
-      // 0x43uu0000 is 128 + u
-      const float c0 = __uint_as_float(prmt(b, 0x43000000u, (i & 1) ? 0x7244u : 0x7044u));
-      const float c1 = __uint_as_float(prmt(b, 0x43000000u, (i & 1) ? 0x7344u : 0x7144u));
-      const float w0 = fmaf(s.s, c0, s.z), w1 = fmaf(s.s, c1, s.z);
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(w1), "f"(w0));
+      // 0x43uu0000 is 128 + u; two weights at a time, code = 128 + u - 136
+      float2 v = make_float2(__uint_as_float(prmt(b, 0x43000000u, (i & 1) ? 0x7244u : 0x7044u)),
+                             __uint_as_float(prmt(b, 0x43000000u, (i & 1) ? 0x7344u : 0x7144u)));
+      v = f32x2_fma(f32x2_add(v, make_float2(-136.0f, -136.0f)), make_float2(s.s, s.s), make_float2(s.z, s.z));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(v.y), "f"(v.x));
     }
   } else {
     o[0] = bf16x2_minus136(prmt(L, 0x43434343u, 0x5140u));

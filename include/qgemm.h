@@ -426,7 +426,8 @@ int qconv2d_f32_dyn_a8w4(int Nb, int H, int W, int Cin, int Cout, int KH, int KW
  * N >= 1.  No workspace.
  * Sums are held in f32 and y is rounded once.
  *   Many rows: each weight w[n,k] is rounded to bf16 first (half a step,
- *   2^-8 of it).
+ *   2^-8 of it; less than 2^-15 of it more comes from f32 scales in two bf16
+ *   parts, 2^-24 from the f32 sum sw*c + zw).
  *   A few rows (up to 16, up to 4 per expert on average): the codes are used
  *   exactly, as c + 136 in sums that start at -136 * sum_k x over the group.
  *   That costs the group's f32 sum about 5 of its 24 bits, and a group whose
