@@ -630,6 +630,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       int s = (it & 1) == group ? 0 : 1;  // this group's stages: every other one
       RawScales now = fetch(s), next = fetch(s + 2);
       for (; s < stages; s += 2) {
+        // The first copies leave ahead of the work before this call and find
+        // free slots; every later one follows it, and so must the count of a
+        // bounded wait for it or for its slot.
+        if (early && it + s >= NRING) {
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          early = false;
+        }
         ok = warp_wait(&n_full[nib], npar, status);
         if (!ok) break;
         uint32_t wd[8];
@@ -658,10 +665,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         now = next;
         next = fetch(s + 4);
-        if (early && par == 0) {  // from here on a wait can block
-          asm volatile("griddepcontrol.wait;" ::: "memory");
-          early = false;
-        }
         ok = warp_wait(&empty[free], par, status);  // the first round passes
         if (!ok) break;
         const uint32_t dst = w_at + slot * (SUBS * W_BYTES);
