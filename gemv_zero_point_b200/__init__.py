@@ -189,8 +189,8 @@ def qg_device_status(reset=True):
 
 def qg_test_arm_stall(which):
     """Test hook: arm one stalled pipeline for the next launch of a kernel
-    family (1 = INT8 GEMM one-CTA kernel, 2 = A8W4 tensor-core kernel, 0 =
-    disarm); see include/qgemm.h."""
+    family (1 = INT8 GEMM one-CTA kernel, 2 = A8W4 tensor-core kernel, 3 =
+    weight-only int4 kernel for many rows, 0 = disarm); see include/qgemm.h."""
     _check(lib.qg_test_arm_stall(int(which)), "qg_test_arm_stall")
 
 

@@ -27,6 +27,7 @@ struct A16W4Call {
   int64_t ld_out;
 };
 constexpr int kA16W4MaxExperts = 1024;
+constexpr int kStallA16W4TC = 3;  // the kernel for many rows, beside StallTarget's
 constexpr int kA16W4MaxSide = 1 << 24;  // N and K, either of which is a reduction
 int launch_a16w4_rows(const A16W4Call& c, cudaStream_t st);           // few rows (a16w4.cu)
 // many rows (a16w4_tc.cu); indirect rows need a workspace to be sorted in

@@ -108,6 +108,8 @@ struct TcArgs {
   int ftiles, stages, subs;  // subs: sub-tiles of the reduction
   int splits;        // kShared: CTAs of a cluster
   int whole;         // the reduction is whole sub-tiles: rows as [64-wide block][row][64]
+  int stall;         // test hook: no rows are asked for for a CTA's second stage
+  uint32_t spin;     // limit of the pipeline's waits
 };
 
 struct Tile {
@@ -211,8 +213,7 @@ __device__ __forceinline__ bool elect_one() {
 
 // Every lane waits; the warp takes its decision together.  The limit counts
 // the pipeline's own time: a role waits for the work before this call first.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status,
-                                          uint32_t limit = kSpinLimit) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, uint32_t limit) {
   // a phase that is complete is seen at once; a parked wait costs about 180
   // cycles even then
   if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
@@ -466,10 +467,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t sub_b = (uint32_t)box_rows(box) * (KS * 2);  // bytes of a sub-tile
       const void* map = &maps.rows[box];
       for (int s = 0; s < stages; ++s, ++it) {
-        ok = warp_wait(&empty[free], par, status);  // the first round passes
+        ok = warp_wait(&empty[free], par, status, a.spin);  // the first round passes
         if (!ok) break;
         const int subs = a.whole ? SUBS : min(SUBS, a.subs - SUBS * (s_first + s));
-        if (elect_one()) {
+        if (!(a.stall && it == 1) && elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[slot], sub_b * (uint32_t)(PAIR ? 2 * subs : subs));
           const uint32_t dst = sX + slot * (SUBS * X_BYTES);
           const uint32_t bar = PAIR ? mapa(smem_u32(&full[slot]), 0) : smem_u32(&full[slot]);
@@ -491,8 +492,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Every copy has landed (in a pair the first CTA waits for both, and the
     // CTAs end together) and every commit has arrived before the CTA may exit.
     for (uint32_t k = it > STAGES ? it - STAGES : 0; k < it; ++k) {
-      if (rank == 0) warp_wait(&full[k % STAGES], (k / STAGES) & 1, status);
-      if (ok) warp_wait(&empty[k % NBAR], (k / NBAR) & 1, status);
+      if (rank == 0 && !(a.stall && k == 1)) warp_wait(&full[k % STAGES], (k / STAGES) & 1, status, kSpinLimit);
+      if (ok) warp_wait(&empty[k % NBAR], (k / NBAR) & 1, status, a.spin);
     }
   } else if (warp == 2) {
     // ---------------- nibbles (inputs of the call alone) ----------------
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       for (int s = 0; s < stages; ++s, ++it) {
         if (it == NRING) asm volatile("griddepcontrol.wait;" ::: "memory");  // from here on a wait can block
-        ok = warp_wait(&n_empty[slot], par, status);  // the first round passes
+        ok = warp_wait(&n_empty[slot], par, status, a.spin);  // the first round passes
         if (!ok) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&n_full[bar], NIB_BYTES);
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     for (uint32_t k = it > NRING ? it - NRING : 0; k < it; ++k)
-      warp_wait(&n_full[k % NBAR], (k / NBAR) & 1, status);
+      warp_wait(&n_full[k % NBAR], (k / NBAR) & 1, status, kSpinLimit);
   } else if (warp == 1) {
     // ---------------- MMA issue ----------------
     // One thread, and every stage passes through it: with divisions by the
@@ -553,10 +554,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                                ((uint32_t)((PAIR ? 2 * TF : TF) >> 4) << 24);
         const uint32_t buf = use & 1;
         const uint32_t next_x = (uint32_t)box_rows(box_of(PAIR ? n / 2 : n)) * (KS * 2) >> 4;
-        ok = warp_wait(&t_empty[buf], ((use >> 1) & 1) ^ 1, status);
+        ok = warp_wait(&t_empty[buf], ((use >> 1) & 1) ^ 1, status, a.spin);
         const uint32_t d = tmem_base + buf * TT;
         for (int s = 0; s < stages && ok; ++s) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], par, status));
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], par, status, a.spin));
           if (!ok) break;
           tc_fence_after();
           const int subs = min(SUBS, a.subs - SUBS * (s_first + s));
@@ -588,11 +589,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (ok) {  // the epilogues' last signals have arrived, the other CTA's among them
         for (uint32_t k = use > 2 ? use - 2 : 0; k < use; ++k)
-          warp_wait(&t_empty[k & 1], (k >> 1) & 1, status);
+          warp_wait(&t_empty[k & 1], (k >> 1) & 1, status, a.spin);
       } else {  // MMAs in flight end before their operands or TMEM go away
         if (elect_one()) commit<PAIR>(drain);
         __syncwarp();
-        warp_wait(drain, 0, status);
+        warp_wait(drain, 0, status, kSpinLimit);
       }
     }
   } else if (warp >= CONV_WARP0) {
@@ -637,7 +638,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           asm volatile("griddepcontrol.wait;" ::: "memory");
           early = false;
         }
-        ok = warp_wait(&n_full[nib], npar, status);
+        ok = warp_wait(&n_full[nib], npar, status, a.spin);
         if (!ok) break;
         uint32_t wd[8];
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         now = next;
         next = fetch(s + 4);
-        ok = warp_wait(&empty[free], par, status);  // the first round passes
+        ok = warp_wait(&empty[free], par, status, a.spin);  // the first round passes
         if (!ok) break;
         const uint32_t dst = w_at + slot * (SUBS * W_BYTES);
 #pragma unroll
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Tile tl = tile_at(t);
       const uint32_t buf = use & 1;
       // a whole reduction, of 2^24 at most
-      if (!warp_wait(&t_full[buf], (use >> 1) & 1, status, kSpinLimit << 4)) break;
+      if (!warp_wait(&t_full[buf], (use >> 1) & 1, status, a.spin << 4)) break;
       tc_fence_after();
       const int f = tl.f0 + 32 * q + lane;
       float b = 0.0f;
@@ -973,6 +974,8 @@ int launch_a16w4_tc(const A16W4Call& call, bool grad, void* ws, cudaStream_t st)
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return QG_ERR_CUDA;
   TcArgs a{};
   a.c = c;
+  a.stall = take_stall(kStallA16W4TC);
+  a.spin = a.stall ? kStallSpinLimit : kSpinLimit;
   a.F = grad ? c.K : c.N;
   a.R = grad ? c.N : c.K;
   a.subs = (int)cdiv(a.R, KS);

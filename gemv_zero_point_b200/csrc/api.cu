@@ -8,6 +8,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "a16w4.cuh"
 #include "qg_internal.cuh"
 
 namespace qg {
@@ -168,7 +169,7 @@ extern "C" int qg_device_status(int reset) {
 }
 
 extern "C" int qg_test_arm_stall(int which) {
-  if (which != kStallNone && which != kStallInt8Gemm && which != kStallA8W4TC)
+  if (which != kStallNone && which != kStallInt8Gemm && which != kStallA8W4TC && which != kStallA16W4TC)
     return QG_ERR_INVALID_ARG;
   g_stall_armed.store(which);
   return QG_OK;

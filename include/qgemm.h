@@ -87,6 +87,8 @@ int qg_device_status(int reset);
  *   which: 1 = INT8 GEMM one-CTA kernel (a call with K > 128 and M <= 128, or
  *              M <= 256 when its 128 x 256 tiles fit in one wave of SMs),
  *          2 = A8W4 tensor-core kernel (an M > 1 call that takes it),
+ *          3 = weight-only int4 kernel for many rows (a call that takes it, with
+ *              two stages of 128 of the reduction or more for a CTA),
  *          0 = disarm.
  * Returns QG_OK, or QG_ERR_INVALID_ARG for another value.  Not for
  * production use: one process-wide flag, taken by whichever thread launches
