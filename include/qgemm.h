@@ -435,7 +435,9 @@ int qconv2d_f32_dyn_a8w4(int Nb, int H, int W, int Cin, int Cout, int KH, int KW
  *   That costs the group's f32 sum about 5 of its 24 bits, and a group whose
  *   sum |x| reaches 2^120 overflows.
  * Rows of x do not mix: a non-finite value in one row reaches that row of y
- * alone, which is then NaN or infinite there.
+ * alone.  Many rows, and gradients, follow the formula there (an infinite x[k]
+ * gives an infinity of w[n,k]'s sign); with a few rows the value is NaN or
+ * infinite, since an infinity is part of the sums that start at -136 * sum x.
  * ------------------------------------------------------------------------ */
 typedef enum {
   QG_W4_F32 = 0,  /* pack_w4_g32: f32 group scales */

@@ -97,3 +97,23 @@ def routing(rng, T, topk, E, drop=0.0, hot=None):
 
 def real(qw, sw, zw):
     return oracle.w4_values(qw, sw, zw)
+
+
+def integer_rows(rng, M, K):
+    """Rows of whole numbers in [-8, 8], bf16 values exactly."""
+    return rng.integers(-8, 9, (M, K)).astype(np.float32)
+
+
+def exact_codes_tolerance(x, qw, sw, zw, ref, bias=None):
+    """Bound on |y - ref| where the codes are used exactly (few rows) and x are
+    integer_rows.  A group's products (c + 136) x and its -136 X are whole
+    numbers whose sums stay below 32 * 8 * (143 + 136) < 2^24, so the group's sum
+    is exact in f32 in whatever order.  What is rounded, by 2^-24 of at most
+    A = sum |sw c x| + sum |zw x| + |b| each time: the product with sw in its sum,
+    the factor -1/136, its product with zw and that one's sum (four a group),
+    the sum of eight warps and the bias.  Then half a step of the output."""
+    A = np.abs(x) @ np.abs(real(qw, sw, None)).T + (0.0 if bias is None else np.abs(bias))
+    if zw is not None:
+        A = A + np.abs(x) @ np.repeat(np.abs(zw.astype(np.float64)), 32, axis=1).T
+    inner = (4 * (qw.shape[1] // 32) + 9) * 2.0 ** -24 * A
+    return inner + 2.0 ** -8 * (np.abs(ref) + inner) + 1e-30
