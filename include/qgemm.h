@@ -426,7 +426,10 @@ int qconv2d_f32_dyn_a8w4(int Nb, int H, int W, int Cin, int Cout, int KH, int KW
  *   bias: f32 [N] or NULL;  y: bf16 [M][ldy] (ldy >= N), any alignment
  * K % 64 == 0, N and K <= 16777216 (else QG_ERR_UNSUPPORTED); M >= 0, any
  * N >= 1.  No workspace.
- * Sums are held in f32 and y is rounded once.
+ * Sums are held in f32 and y is rounded once.  With many rows, and in
+ * gradients, the tensor cores take 16 terms at a time and cut the sum off
+ * towards zero, each time by less than 2^-23 of it: together less than half a
+ * step of y (2^-8) for reductions up to 2^19, up to 2^-3 of y at 2^24.
  *   Many rows: each weight w[n,k] is rounded to bf16 first (half a step,
  *   2^-8 of it; less than 2^-15 of it more comes from f32 scales in two bf16
  *   parts, 2^-24 from the f32 sum sw*c + zw).

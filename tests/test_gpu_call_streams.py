@@ -112,6 +112,22 @@ def test_workspace_belongs_to_the_calls_stream(lib, monkeypatch, kind, raw):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("kind", CALLS)
+def test_the_default_stream_by_its_handle(lib, kind):
+    """Handle 0 is the default stream, not the current one."""
+    call = kind(lib, 4)
+    call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in call.result()]
+    for t in call.result():
+        t.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        call(stream=0)
+        torch.cuda.default_stream().synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(call.result(), want))
+
+
 def test_packed_weights_of_another_stream(lib, monkeypatch):
     """A matrix packed on another stream: its memory is not handed out before
     that stream, or the current one, is done with it."""
