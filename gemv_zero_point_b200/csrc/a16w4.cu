@@ -19,9 +19,11 @@
 //     by MMAs with the constant once per chunk for all weight rows.
 //   - The group scale is applied to the f32 sums of the group: nothing is
 //     rounded below f32 before y (the 136 costs the sums 5 of their 24 bits).
-// 1x14336x4096 takes 12.4 us (2.96 TB/s), 12x4096x14336 19.7 us, 8 tokens x 8
-// of 64 experts of 2048x2048 38 us.  42 to 49 % of the issue slots are used;
-// the chains of a chunk (ldmatrix, unpacking, MMAs, scales) leave the rest.
+// 1x14336x4096 takes 12.4 us (2.96 TB/s), 12x4096x14336 19.0 us, 8 tokens x 8
+// of 64 experts of 2048x2048 35 to 40 us, by how many of them the tokens reach.
+// 42 to 49 % of the issue slots are used; the chains of a chunk (ldmatrix,
+// unpacking, MMAs, scales) leave the rest.  At the 128 registers that two CTAs
+// an SM allow, the forms for 8 tokens spill 24 to 184 bytes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

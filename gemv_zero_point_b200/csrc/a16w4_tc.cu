@@ -27,9 +27,11 @@
 // operands go through slower registers: 415 against 352 us at
 // 4096x14336x4096).  Per stage of a full tile 64 KB of weights and 64 KB of
 // rows go in and out of shared memory, 1024 cycles at its rate, as long as the
-// MMAs: 4096x14336x4096 takes 312 us (1540 TFLOP/s, tensor pipe 92 % of the
-// busy cycles), 64x14336x4096 22 us (about 1000 cycles a stage, half of them
-// the weights' way through shared memory).
+// MMAs: 4096x14336x4096 with bf16 scales takes 318 us in a burst at 1965 MHz
+// (1510 TFLOP/s, tensor pipe 92 % of the busy cycles) and 370 us back to back
+// for seconds, where the power limit holds the clock at 1340 MHz (1300 TFLOP/s);
+// 64x14336x4096 takes 21 us (about 1000 cycles a stage, half of them the
+// weights' way through shared memory).
 //
 // Both directions read the same 128 rows n x 128 k of the packed matrix per
 // stage.  Forward the bf16 sub-tiles are K-major; for the gradient the
@@ -45,9 +47,9 @@
 //   warps 8-23  expansion of the nibbles into the swizzled bf16 stage, two
 //               groups of eight warps that take the stages in turn (one stage
 //               takes a group about 700 cycles, mostly latencies)
-// Indirect rows are first brought into sorted order in the workspace (about
-// 24 us for 32768 rows of 2048, 215 us in all with 64 experts of 1536
-// features): gathering them here took 963 us in all with tensor-map row
+// Indirect rows are first brought into sorted order in the workspace (24 us
+// for 32768 rows of 2048, 215 us in all with 64 experts of 1536 features):
+// gathering them here took 963 us in all with tensor-map row
 // gathers of four rows, 534 with cp.async.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -537,9 +537,9 @@ int run_combine_grad_as(int T_, int topk, int64_t S, int N, const void* dy, int6
 
 // go(V, J), both as types, for `vec` values per access and the experts per
 // step.  4096 tokens of 4096 bf16: topk 4 summed 8 at a time 41.6 us, 4 at a
-// time 32.6; topk 2 36.5 and, 2 at a time, 21.1 (rows of 4091: 68 and 46).
+// time 32.6; topk 2 36.5 and, 2 at a time, 18.4 (rows of 4091: 68 and 46).
 // With few tokens and narrow accesses a thread with 8 to 16 of them only lasts
-// longer than several threads with 4 (1 token, 2 x 2001: 2.2 and 1.9 us).
+// longer than several threads with 4 (1 token, 2 x 2001: 2.2 and 1.7 us).
 template <typename T, typename F>
 int by_shape(int vec, int T_, int topk, F go) {
   constexpr int B = (int)sizeof(T);
