@@ -573,7 +573,8 @@ def qgemm_a16w4_bf16(x, packed_w, y, bias=None, weights="f32", stream=None):
 def qgemm_a16w4_bf16_experts(x, offsets, packed_w, y, src=None, topk=1, bias=None, weights="f32",
                              workspace=None, stream=None):
     """y[p] = W[e] @ x[src[p] // topk] + bias[e] (x[p] without src) for the rows
-    p of expert e, offsets[e] <= p < offsets[e+1]; packed_w uint8 [E][bytes]."""
+    p of expert e, offsets[e] <= p < offsets[e+1]; packed_w uint8 [E][bytes], a
+    multiple of 16 bytes from one matrix to the next."""
     torch = _torch()
     fmt = _w4_format(weights)
     rows, K, ldx = _rows(x, torch.bfloat16, "x")

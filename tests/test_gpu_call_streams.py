@@ -228,3 +228,55 @@ def test_steps_behind_one_another_share_their_buffers(lib, T, topk, N, grad):
             # f32 sums of topk products, rounded to bf16
             ref, A = wd.sum(2)[..., None] * xd, wd.sum(2)[..., None] * xd.abs()
             assert ((y.double() - ref).abs() <= (2.0 ** -8 + topk * 2.0 ** -22) * A + 1e-30).all()
+
+
+def test_every_call_on_three_streams_at_once(lib):
+    """Few and many rows, dense and per expert, gradients, order and rows, each
+    stream in its own order: the bits of the calls one after the other."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rng = np.random.default_rng(8)
+    E, N, K, T, topk = 6, 200, 320, 150, 2
+    qw, sw, zw = C.weights(rng, N, K, "asym", E)
+    packed = C.pack_experts(lib, torch, qw, sw, zw, "asym")
+
+    def lane(k):
+        rows = torch.randn((T * topk, K), generator=g, device="cuda").to(BF)
+        dys = torch.randn((T * topk, N), generator=g, device="cuda").to(BF)
+        ids = torch.randint(0, E, (T, topk), generator=g, device="cuda", dtype=torch.int32)
+        w = torch.rand((T, topk), generator=g, device="cuda")
+        o = {"off": _i32(np.zeros(E + 1)), "src": _i32(np.zeros(T * topk)), "pos": _i32(np.zeros((T, topk)))}
+        for name, shape in [("few", (9, N)), ("many", (T, N)), ("grad", (T, K)), ("h", (T * topk, N)),
+                            ("dx", (T * topk, K)), ("y", (T, N)), ("dh", (T * topk, N)), ("xs", (T * topk, K))]:
+            o[name] = torch.zeros(shape, dtype=BF, device="cuda")
+        o["dw"] = torch.zeros((T, topk), device="cuda")
+
+        def run(s):
+            lib.qg_sort_by_expert(ids, o["off"], o["src"], o["pos"], stream=s)
+            lib.qgemm_a16w4_bf16_experts(rows[:T], o["off"], packed, o["h"], src=o["src"], topk=topk,
+                                         weights="asym", stream=s)
+            lib.qg_combine_rows(o["h"], o["pos"], o["y"], weights=w, stream=s)
+            lib.qgemm_a16w4_bf16(rows[:9], packed[k], o["few"], weights="asym", stream=s)
+            lib.qgemm_a16w4_bf16(rows[:T], packed[k], o["many"], weights="asym", stream=s)
+            lib.qg_combine_rows_grad(o["many"], o["h"], o["pos"], w, o["dh"], o["dw"], stream=s)
+            lib.qgemm_a16w4_bf16_grad_x(dys[:T], packed[k], o["grad"], weights="asym", stream=s)
+            lib.qgemm_a16w4_bf16_experts_grad_x(o["dh"], o["off"], packed, o["dx"], weights="asym", stream=s)
+            lib.qg_spread_rows(o["grad"], o["pos"], o["xs"], stream=s)
+        return run, o
+
+    lanes = [lane(k) for k in range(3)]
+    want = []
+    for run, o in lanes:
+        run(None)
+        torch.cuda.synchronize()
+        want.append({k: t.clone() for k, t in o.items()})
+    streams = [torch.cuda.Stream() for _ in lanes]
+    for k in range(30):
+        for (run, o), s in zip(lanes, streams):
+            run(s)
+        if k % 10 == 9:
+            torch.cuda.synchronize()
+            for (_, o), ref in zip(lanes, want):
+                for name, t in o.items():
+                    assert torch.equal(t, ref[name]), (k, name)
+                    t.zero_()
+            torch.cuda.synchronize()
